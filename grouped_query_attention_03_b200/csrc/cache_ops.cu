@@ -1,0 +1,191 @@
+// cache_ops.cu -- gqa_tree_commit and gqa_cache_evict: argument checks and
+// launches.
+#include <algorithm>
+
+#include "evict.cuh"
+#include "host.cuh"
+#include "tree_commit.cuh"
+
+namespace {
+
+using namespace gqa::host;
+
+// Vectors a row is moved in: 16 bytes where rows and buffers allow, else
+// elements.
+struct RowVec {
+  int bytes;  // of one vector
+  int vpr;    // vectors per row
+};
+
+RowVec row_vec(gqa_dtype dtype, int d, std::initializer_list<const void *> ptrs) {
+  const int esz = dtype == GQA_F32 ? 4 : 2;
+  bool ok = (int64_t)d * esz % 16 == 0;
+  for (const void *p : ptrs) ok = ok && aligned16(p);
+  return ok ? RowVec{16, d * esz / 16} : RowVec{esz, d};
+}
+
+// Columns a tree commit may move with one cluster of 8 CTAs and still hide
+// behind its latency; larger in-place commits take the whole GPU and a
+// second launch for the lengths.
+constexpr int64_t kClusterCols = 32768;
+
+template <typename V>
+gqa_status launch_commit(void *kc, void *vc, const void *kd, const void *vd,
+                         gqa::tree::CommitParams p, int sms, cudaStream_t st) {
+  const int64_t cols = (int64_t)2 * p.B * p.Hkv * p.vpr;
+  const bool apart = p.lens_out != p.seq_lens;
+  const bool cluster = !apart && cols <= kClusterCols;
+  const int64_t want = (cols + 255) / 256;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(cluster ? std::min<int64_t>(want, 8)
+                                        : std::min<int64_t>(want, (int64_t)sms * 8)));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cfg.gridDim.x;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster ? 2 : 1;
+  const int commit = apart || cluster ? 1 : 0;
+  gqa_status s = launched(cudaLaunchKernelEx(&cfg, gqa::tree::tree_commit_kernel<V>, (V *)kc,
+                                             (V *)vc, (const V *)kd, (const V *)vd, p, commit,
+                                             cluster ? 1 : 0));
+  if (s != GQA_OK || commit) return s;
+  return launched(gqa::launch_dependent(gqa::tree::tree_commit_lens_kernel, dim3(1), dim3(256), 0,
+                                        st, p));
+}
+
+template <typename V>
+gqa_status launch_evict_rows(const void *kc, const void *vc, void *ko, void *vo,
+                             const gqa::evict::Params &p, int vpr, bool in_place, int sms,
+                             cudaStream_t st) {
+  if (in_place) {
+    // slices of 64 bytes (4 vectors): a whole DRAM burst each, and 8 CTAs a
+    // lane for a 256-byte row of K and V
+    constexpr int SL = sizeof(V) == 16 ? 4 : 32;
+    const int slices = (vpr + SL - 1) / SL;
+    const int64_t grid = (int64_t)p.B * p.Hkv * 2 * slices;
+    if (grid > INT_MAX) return GQA_ERR_UNSUPPORTED;
+    return launched(gqa::launch_dependent(gqa::evict::evict_move_kernel<V, SL>,
+                                          dim3((unsigned)grid), dim3(256), 0, st, (V *)ko,
+                                          (V *)vo, p, vpr, slices));
+  }
+  const int64_t total = (int64_t)p.B * p.Hkv * p.budget * vpr;
+  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>((total + 1023) / 1024, (int64_t)sms * 8));
+  return launched(gqa::launch_dependent(gqa::evict::evict_copy_kernel<V>, dim3((unsigned)grid),
+                                        dim3(256), 0, st, (const V *)kc, (const V *)vc, (V *)ko,
+                                        (V *)vo, p, vpr));
+}
+
+}  // namespace
+
+extern "C" {
+
+gqa_status gqa_tree_commit(gqa_dtype dtype, void *k_cache, void *v_cache, const void *k_draft,
+                           const void *v_draft, const int32_t *path, const int32_t *path_lens,
+                           const int32_t *seq_lens, int32_t *lens_out, int B, int Hkv, int C,
+                           int d, int t_new, int max_path, int32_t *dev_status,
+                           gqa_stream_t stream) {
+  if (dtype != GQA_F32 && dtype != GQA_BF16) return GQA_ERR_UNSUPPORTED;
+  if (B < 0 || C < 0 || t_new < 0 || max_path < 0) return GQA_ERR_SHAPE;
+  if (Hkv <= 0 || d <= 0) return GQA_ERR_SHAPE;
+  int64_t nc, nd, np;
+  if (!elems(&nc, {B, Hkv, C, d}) || !elems(&nd, {B, Hkv, t_new, d}) ||
+      !elems(&np, {B, max_path}) || nc > INT64_MAX / 8 || nd > INT64_MAX / 8)
+    return GQA_ERR_OVERFLOW;
+  if (B == 0) return GQA_OK;
+  if (!path_lens || !seq_lens || !lens_out || !dev_status) return GQA_ERR_NULL;
+  if (C > 0 && (!k_cache || !v_cache)) return GQA_ERR_NULL;
+  if (t_new > 0 && max_path > 0 && (!k_draft || !v_draft || !path)) return GQA_ERR_NULL;
+  DeviceInfo di;
+  gqa_status s = device_info(&di);
+  if (s != GQA_OK) return s;
+  const RowVec rv = row_vec(dtype, d, {k_cache, v_cache, k_draft, v_draft});
+  gqa::tree::CommitParams p;
+  p.path = path;
+  p.path_lens = path_lens;
+  p.seq_lens = seq_lens;
+  p.lens_out = lens_out;
+  p.status = dev_status;
+  p.B = B;
+  p.Hkv = Hkv;
+  p.C = C;
+  p.t_new = t_new;
+  p.P = max_path;
+  p.vpr = rv.vpr;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (rv.bytes == 16)
+    return launch_commit<uint4>(k_cache, v_cache, k_draft, v_draft, p, di.sms, st);
+  if (rv.bytes == 4)
+    return launch_commit<uint32_t>(k_cache, v_cache, k_draft, v_draft, p, di.sms, st);
+  return launch_commit<uint16_t>(k_cache, v_cache, k_draft, v_draft, p, di.sms, st);
+}
+
+gqa_status gqa_cache_evict(gqa_dtype dtype, const void *k_cache, const void *v_cache,
+                           const float *weights, const int32_t *seq_lens, void *k_out,
+                           void *v_out, float *weights_out, int32_t *lens_out, int32_t *kept,
+                           int B, int Hkv, int C, int C_out, int d, int budget, int recent,
+                           int32_t *dev_status, gqa_stream_t stream) {
+  if (dtype != GQA_F32 && dtype != GQA_BF16) return GQA_ERR_UNSUPPORTED;
+  if (B < 0 || C < 0 || C_out < 0 || budget < 0 || recent < 0) return GQA_ERR_SHAPE;
+  if (Hkv <= 0 || d <= 0) return GQA_ERR_SHAPE;
+  if (recent > budget || budget > C_out) return GQA_ERR_CAPACITY;
+  int64_t nc, no;
+  if (!elems(&nc, {B, Hkv, C, d}) || !elems(&no, {B, Hkv, C_out, d}) || nc > INT64_MAX / 8 ||
+      no > INT64_MAX / 8)
+    return GQA_ERR_OVERFLOW;
+  if (B == 0) return GQA_OK;
+  // nothing to read, or nothing to keep and no weights to clear: the lengths
+  // are still to be written, so the kernels run
+  if (!seq_lens || !lens_out || !dev_status) return GQA_ERR_NULL;
+  if (C > 0 && (!k_cache || !v_cache || !weights)) return GQA_ERR_NULL;
+  if (C_out > 0 && (!k_out || !v_out || !weights_out)) return GQA_ERR_NULL;
+  if (budget > 0 && !kept) return GQA_ERR_NULL;
+  // in place: all three buffers, and of the same capacity
+  const bool in_place = k_out == k_cache;
+  if ((v_out == v_cache) != in_place || (weights_out == weights) != in_place ||
+      (in_place && C != C_out))
+    return GQA_ERR_SHAPE;
+  if (C > (1 << 30) || C_out > (1 << 30)) return GQA_ERR_UNSUPPORTED;
+  if ((int64_t)B * Hkv > INT_MAX) return GQA_ERR_UNSUPPORTED;
+  DeviceInfo di;
+  gqa_status s = device_info(&di);
+  if (s != GQA_OK) return s;
+  gqa::evict::Params p;
+  p.w = weights;
+  p.w_out = weights_out;
+  p.seq_lens = seq_lens;
+  p.lens_out = lens_out;
+  p.kept = kept;
+  p.status = dev_status;
+  p.B = B;
+  p.Hkv = Hkv;
+  p.C = C;
+  p.C_out = C_out;
+  p.budget = budget;
+  p.recent = recent;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const dim3 grid((unsigned)(B * Hkv)), block(gqa::evict::kSelThreads);
+  // Keys in registers up to 32 per thread (the 64 registers that 1024
+  // threads have); fewer when the capacity is small, for fewer compares.
+  cudaError_t e;
+  if (C <= 8 * gqa::evict::kSelThreads)
+    e = gqa::launch_dependent(gqa::evict::evict_select_kernel<8>, grid, block, 0, st, p);
+  else if (C <= 32 * gqa::evict::kSelThreads)
+    e = gqa::launch_dependent(gqa::evict::evict_select_kernel<32>, grid, block, 0, st, p);
+  else
+    e = gqa::launch_dependent(gqa::evict::evict_select_kernel<0>, grid, block, 0, st, p);
+  if ((s = launched(e)) != GQA_OK) return s;
+  const RowVec rv = row_vec(dtype, d, {k_cache, v_cache, k_out, v_out});
+  if (rv.bytes == 16)
+    return launch_evict_rows<uint4>(k_cache, v_cache, k_out, v_out, p, rv.vpr, in_place, di.sms, st);
+  if (rv.bytes == 4)
+    return launch_evict_rows<uint32_t>(k_cache, v_cache, k_out, v_out, p, rv.vpr, in_place, di.sms, st);
+  return launch_evict_rows<uint16_t>(k_cache, v_cache, k_out, v_out, p, rv.vpr, in_place, di.sms, st);
+}
+
+}  // extern "C"

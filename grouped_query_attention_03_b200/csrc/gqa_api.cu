@@ -10,12 +10,12 @@
 #include <climits>
 #include <cstdint>
 #include <cstring>
-#include <mutex>
 
 #include "../../include/gqa.h"
 #include "append.cuh"
 #include "common.cuh"
 #include "decode_splitk.cuh"
+#include "host.cuh"
 #include "prefill_pair.cuh"
 #include "prefill_persist.cuh"
 #include "prefill_split.cuh"
@@ -24,6 +24,7 @@
 namespace {
 
 using bf16 = __nv_bfloat16;
+using namespace gqa::host;
 
 constexpr int kMaxDecodeCtas = gqa::dec::kMaxCtas;  // workspace is sized for this many
 #ifndef GQA_DEC_MIN_ROWS
@@ -40,12 +41,6 @@ constexpr int kDecodeMinRows = GQA_DEC_MIN_ROWS;
 // non-empty lane this many bytes of virtual rows (see dec::extent).
 constexpr int kDecodeLanePadBytes = GQA_DEC_LANE_PAD_BYTES;
 
-
-struct DeviceInfo {
-  int sms = 0;
-  int major = 0;
-};
-
 // The paired prefill kernel's grid for a plain prompt leaves SMs idle and
 // its longest query tile (the last one) walks more than 4 KV tiles: one
 // head per CTA is faster there (see the dispatch in attend_impl).
@@ -59,66 +54,6 @@ bool prefill_prefers_split(int B, int Hq, int Hkv, int Tq, int Tk, int cached, b
   const long long hi = Tq - 1;
   const long long lo = window > 0 ? std::max(0LL, a0 - (window - 1)) : 0;
   return hi / 128 - lo / 128 + 1 > 4;
-}
-
-gqa_status device_info(DeviceInfo *out) {
-  static std::mutex mu;
-  static DeviceInfo cache[64];
-  static bool have[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
-    cudaGetLastError();
-    return GQA_ERR_CUDA;
-  }
-  std::lock_guard<std::mutex> lock(mu);
-  if (!have[dev]) {
-    DeviceInfo d;
-    if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) !=
-            cudaSuccess ||
-        cudaDeviceGetAttribute(&d.major, cudaDevAttrComputeCapabilityMajor,
-                               dev) != cudaSuccess) {
-      cudaGetLastError();
-      return GQA_ERR_CUDA;
-    }
-    cache[dev] = d;
-    have[dev] = true;
-  }
-  *out = cache[dev];
-  return out->major == 10 ? GQA_OK : GQA_ERR_DEVICE;
-}
-
-// a*b*... in int64 with overflow detection (all factors >= 0).
-bool mul_ok(int64_t *acc, int64_t f) {
-  if (f < 0) return false;
-  if (f != 0 && *acc > INT64_MAX / f) return false;
-  *acc *= f;
-  return true;
-}
-
-bool elems(int64_t *out, std::initializer_list<int64_t> dims) {
-  int64_t acc = 1;
-  for (int64_t d : dims)
-    if (!mul_ok(&acc, d)) return false;
-  *out = acc;
-  return true;
-}
-
-bool aligned16(const void *p) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
-}
-
-gqa_status check_heads(int Hq, int Hkv, int d) {
-  if (Hq <= 0 || Hkv <= 0 || d <= 0) return GQA_ERR_SHAPE;
-  if (Hq % Hkv != 0) return GQA_ERR_GROUPS;
-  return GQA_OK;
-}
-
-gqa_status check_window(int window) {
-  return (window == 0 || window < -1) ? GQA_ERR_WINDOW : GQA_OK;
-}
-
-gqa_status launch_status() {
-  return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
 int next_pow2(int x) {
@@ -147,8 +82,6 @@ struct DecLayout {
   size_t counters = 0, ml = 0, acc = 0, total = 0;
   size_t counter_bytes = 0;
 };
-
-size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Workspace: the arrival counters (one per possible first CTA of a split
 // lane, and one count of CTAs that have read the lengths) at a fixed place
@@ -300,6 +233,7 @@ const char *gqa_status_string(gqa_status s) {
     case GQA_ERR_DEVICE: return "current device is not an sm_100 GPU";
     case GQA_ERR_TIMEOUT: return "a bounded wait inside a kernel ran out";
     case GQA_ERR_SEGMENT: return "a packed segment start lies outside [0, t]";
+    case GQA_ERR_TREE: return "a drafted token's parent, or an accepted path, is not valid";
   }
   return "unknown status";
 }

@@ -1,0 +1,254 @@
+// rows.cu -- gqa_decode_tree and gqa_decode_scored: argument checks, the
+// workspace, the choice of kernel, launches.
+#include <algorithm>
+
+#include "host.cuh"
+#include "rows_simt.cuh"
+#include "rows_splitk.cuh"
+
+namespace {
+
+using namespace gqa::host;
+using gqa::rows::Params;
+
+// The workspace is sized for this many CTAs of the tensor-core kernel (one
+// per SM), and the CUDA-core kernel's parts aim at this many CTAs, so that
+// neither depends on the device.
+constexpr int kMaxCtas = 256;
+constexpr int kSimtCtas = 592;
+
+struct Layout {
+  bool tc = false;
+  int NT = 1, group_rows = 0, MG = 1, ns = 0, Cp = 0;
+  int64_t slots = 0;
+  size_t ml = 0, acc = 0, scores = 0, total = 0;
+};
+
+// Sizes only (no pointers): what gqa_decode_*_workspace_bytes can know.  The
+// tensor-core kernel addresses query rows with 32-bit TMA coordinates.
+bool layout(gqa_dtype dtype, int B, int Hq, int Hkv, int C, int d, int t, bool scored, bool tc_ok,
+            Layout *out) {
+  Layout L;
+  int64_t R, rows, lanes, x;
+  if (!elems(&R, {Hq / Hkv, t}) || !elems(&rows, {B, Hq, t}) || !elems(&lanes, {B, Hkv}))
+    return false;
+  if (rows > INT_MAX / 2 || lanes > INT_MAX / 2) return false;
+  L.tc = tc_ok && dtype == GQA_BF16 && (d == 64 || d == 128);
+  if (L.tc) {
+    // up to 128 rows fill one row tile; more are taken in pairs of tiles, so
+    // that two share each K and V tile
+    L.NT = R <= gqa::rows::kM ? 1 : 2;
+    L.MG = (int)((R + 2 * gqa::rows::kM - 1) / (2 * gqa::rows::kM));
+    L.group_rows = L.MG == 1 ? (int)R : 2 * gqa::rows::kM;
+    L.slots = lanes * L.MG + kMaxCtas;
+  } else {
+    L.group_rows = gqa::rows::kSR;
+    L.MG = (int)((R + gqa::rows::kSR - 1) / gqa::rows::kSR);
+    // parts of at least 64 keys, enough of them to fill the GPU
+    const int64_t groups = lanes * L.MG;
+    const int64_t most = std::max<int64_t>(1, ((int64_t)C + t) / 64);
+    L.ns = (int)std::min<int64_t>(std::min<int64_t>(most, 64),
+                                  std::max<int64_t>(1, kSimtCtas / std::max<int64_t>(groups, 1)));
+    L.slots = groups * L.ns;
+  }
+  int64_t n;
+  if (!elems(&n, {L.slots, L.group_rows, 8}) || n > INT64_MAX / 4) return false;
+  L.acc = round256((size_t)n);
+  if (!elems(&n, {L.slots, L.group_rows, d, 4}) || n > INT64_MAX / 4) return false;
+  L.scores = L.acc + round256((size_t)n);
+  L.total = L.scores;
+  if (scored) {
+    if (C > INT_MAX - gqa::rows::kTile) return false;
+    L.Cp = (C + gqa::rows::kTile - 1) / gqa::rows::kTile * gqa::rows::kTile;
+    if (!elems(&x, {lanes, R, L.Cp, 4}) || x > INT64_MAX / 4) return false;
+    L.total += round256((size_t)x);
+  }
+  *out = L;
+  return true;
+}
+
+template <int D, int NT>
+gqa_status launch_tc(const Params &p, const DeviceInfo &di, cudaStream_t st) {
+  using K = gqa::rows::TcCfg<D, NT>;
+  CUtensorMap mq, mk, mv, mkd, mvd;
+  const long long qrows = (long long)p.B * p.Hq * p.t;
+  const int lanes = p.B * p.Hkv;
+  if (!gqa::tma::make_bf16_map(&mq, p.q, D, qrows, 0, 128)) return GQA_ERR_CUDA;
+  if (p.C > 0 && (!gqa::tma::make_bf16_map(&mk, p.k, D, p.C, lanes, 128) ||
+                  !gqa::tma::make_bf16_map(&mv, p.v, D, p.C, lanes, 128)))
+    return GQA_ERR_CUDA;
+  if (p.tree && (!gqa::tma::make_bf16_map(&mkd, p.kd, D, p.t, lanes, 128) ||
+                 !gqa::tma::make_bf16_map(&mvd, p.vd, D, p.t, lanes, 128)))
+    return GQA_ERR_CUDA;
+  // a map that no tile uses stands for its pair
+  if (p.C == 0) {
+    mk = mkd;
+    mv = mvd;
+  }
+  if (!p.tree) {
+    mkd = mk;
+    mvd = mv;
+  }
+  static bool done[64] = {};
+  gqa_status s = allow_smem(gqa::rows::rows_splitk_kernel<D, NT>, K::SMEM, di.id, done);
+  if (s != GQA_OK) return s;
+  return launched(gqa::launch_dependent(gqa::rows::rows_splitk_kernel<D, NT>,
+                                        dim3((unsigned)p.ctas), dim3(K::THREADS), K::SMEM, st, mq,
+                                        mk, mv, mkd, mvd, p));
+}
+
+template <typename T>
+gqa_status launch_simt(const Params &p, const DeviceInfo &di, cudaStream_t st) {
+  const int64_t grid = (int64_t)p.B * p.Hkv * p.MG * p.ns;
+  if (grid > INT_MAX) return GQA_ERR_UNSUPPORTED;
+  static bool done[64] = {};
+  gqa_status s = allow_smem(gqa::rows::rows_simt_kernel<T>, gqa::rows::simt_smem(GQA_MAX_HEAD_DIM),
+                            di.id, done);
+  if (s != GQA_OK) return s;
+  return launched(gqa::launch_dependent(gqa::rows::rows_simt_kernel<T>, dim3((unsigned)grid),
+                                        dim3(gqa::rows::kSimtThreads), gqa::rows::simt_smem(p.d),
+                                        st, p));
+}
+
+struct Operands {
+  const void *q, *k, *v, *kd, *vd;
+  const int32_t *parents, *seq_lens;
+  void *o;
+  float *weights;  // scored
+};
+
+gqa_status rows_impl(gqa_dtype dtype, const Operands &op, bool tree, int B, int Hq, int Hkv, int C,
+                     int d, int t, int window, float scale, void *workspace,
+                     size_t workspace_bytes, int32_t *dev_status, gqa_stream_t stream) {
+  if (dtype != GQA_F32 && dtype != GQA_BF16) return GQA_ERR_UNSUPPORTED;
+  if (B < 0 || C < 0 || t < 0) return GQA_ERR_SHAPE;
+  gqa_status s = check_heads(Hq, Hkv, d);
+  if (s != GQA_OK) return s;
+  if ((s = check_window(window)) != GQA_OK) return s;
+  int64_t nq, nc;
+  if (!elems(&nq, {B, Hq, t, d}) || !elems(&nc, {B, Hkv, C, d}) || nq > INT64_MAX / 8 ||
+      nc > INT64_MAX / 8)
+    return GQA_ERR_OVERFLOW;
+  if (t > GQA_MAX_TREE) return GQA_ERR_UNSUPPORTED;
+  if (!tree && t > C) return GQA_ERR_CAPACITY;
+  if (B == 0 || t == 0) return GQA_OK;
+  if (!op.q || !op.o || !op.seq_lens || !dev_status) return GQA_ERR_NULL;
+  if (C > 0 && (!op.k || !op.v)) return GQA_ERR_NULL;
+  if (tree ? (!op.kd || !op.vd) : !op.weights) return GQA_ERR_NULL;
+  if (d > GQA_MAX_HEAD_DIM) return GQA_ERR_UNSUPPORTED;
+  const bool aligned = aligned16(op.q) && aligned16(op.k) && aligned16(op.v) && aligned16(op.kd) &&
+                       aligned16(op.vd) && aligned16(op.o);
+  // tile coordinates and key indexes are 32-bit
+  if (C > INT_MAX - 2 * GQA_MAX_TREE) return GQA_ERR_UNSUPPORTED;
+  Layout L;
+  if (!layout(dtype, B, Hq, Hkv, C, d, t, !tree, aligned, &L)) return GQA_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < L.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return GQA_ERR_WORKSPACE;
+  DeviceInfo di;
+  if ((s = device_info(&di)) != GQA_OK) return s;
+  unsigned char *ws = static_cast<unsigned char *>(workspace);
+  Params p = {};
+  p.q = op.q;
+  p.k = op.k;
+  p.v = op.v;
+  p.kd = op.kd;
+  p.vd = op.vd;
+  p.parents = op.parents;
+  p.seq_lens = op.seq_lens;
+  p.o = op.o;
+  p.status = dev_status;
+  p.ml = reinterpret_cast<float2 *>(ws + L.ml);
+  p.acc = reinterpret_cast<float *>(ws + L.acc);
+  p.scores = tree ? nullptr : reinterpret_cast<float *>(ws + L.scores);
+  p.weights = op.weights;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.C = C;
+  p.d = d;
+  p.t = t;
+  p.r = Hq / Hkv;
+  p.R = p.r * t;
+  p.window = window;
+  p.tree = tree ? 1 : 0;
+  p.Cp = L.Cp;
+  p.group_rows = L.group_rows;
+  p.MG = L.MG;
+  p.ctas = std::min(kMaxCtas, di.sms);
+  p.min_tiles = 1;
+  p.ns = L.ns;
+  p.scale_log2 = scale * gqa::kLog2e;
+  // the merge's grid, checked before anything is launched
+  const int64_t groups = (int64_t)B * Hkv * L.MG;
+  const int row_blocks = (std::min(L.group_rows, p.R) + 7) / 8;
+  const int cell_blocks = tree ? 0 : (C + gqa::rows::kFinishCells - 1) / gqa::rows::kFinishCells;
+  const bool merges = L.tc || L.ns > 1;
+  const int64_t merge_blocks = merges ? groups * row_blocks : 0;
+  const int64_t grid = merge_blocks + (int64_t)B * Hkv * cell_blocks;
+  if (grid > INT_MAX) return GQA_ERR_UNSUPPORTED;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (L.tc) {
+    if (d == 64)
+      s = L.NT == 1 ? launch_tc<64, 1>(p, di, st) : launch_tc<64, 2>(p, di, st);
+    else
+      s = L.NT == 1 ? launch_tc<128, 1>(p, di, st) : launch_tc<128, 2>(p, di, st);
+  } else {
+    s = dtype == GQA_F32 ? launch_simt<float>(p, di, st) : launch_simt<__nv_bfloat16>(p, di, st);
+  }
+  if (s != GQA_OK || grid == 0) return s;
+  auto *finish = dtype == GQA_F32 ? gqa::rows::rows_finish_kernel<float>
+                                  : gqa::rows::rows_finish_kernel<__nv_bfloat16>;
+  return launched(gqa::launch_dependent(finish, dim3((unsigned)grid),
+                                        dim3(gqa::rows::kFinishThreads), 0, st, p,
+                                        (int)merge_blocks, row_blocks, cell_blocks));
+}
+
+// The larger of the two layouts: buffers that are not 16-byte aligned run
+// the CUDA-core kernel.
+size_t workspace_bytes_of(gqa_dtype dtype, int B, int Hq, int Hkv, int C, int d, int t, bool scored) {
+  if (dtype != GQA_F32 && dtype != GQA_BF16) return 0;
+  if (B < 0 || C < 0 || t < 0 || t > GQA_MAX_TREE || check_heads(Hq, Hkv, d) != GQA_OK) return 0;
+  if (d > GQA_MAX_HEAD_DIM || C > INT_MAX - 2 * GQA_MAX_TREE) return 0;
+  Layout a, b;
+  if (!layout(dtype, B, Hq, Hkv, C, d, t, scored, true, &a) ||
+      !layout(dtype, B, Hq, Hkv, C, d, t, scored, false, &b))
+    return 0;
+  return std::max(a.total, b.total);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gqa_decode_tree_workspace_bytes(gqa_dtype dtype, int B, int Hq, int Hkv, int C, int d,
+                                       int t_new) {
+  return workspace_bytes_of(dtype, B, Hq, Hkv, C, d, t_new, false);
+}
+
+size_t gqa_decode_scored_workspace_bytes(gqa_dtype dtype, int B, int Hq, int Hkv, int C, int d,
+                                         int t_new) {
+  return workspace_bytes_of(dtype, B, Hq, Hkv, C, d, t_new, true);
+}
+
+gqa_status gqa_decode_tree(gqa_dtype dtype, const void *q, const void *k_cache,
+                           const void *v_cache, const void *k_draft, const void *v_draft,
+                           const int32_t *parents, void *o, const int32_t *seq_lens, int B,
+                           int Hq, int Hkv, int C, int d, int t_new, int window, float scale,
+                           void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                           gqa_stream_t stream) {
+  const Operands op{q, k_cache, v_cache, k_draft, v_draft, parents, seq_lens, o, nullptr};
+  return rows_impl(dtype, op, true, B, Hq, Hkv, C, d, t_new, window, scale, workspace,
+                   workspace_bytes, dev_status, stream);
+}
+
+gqa_status gqa_decode_scored(gqa_dtype dtype, const void *q, const void *k_cache,
+                             const void *v_cache, void *o, float *weights,
+                             const int32_t *seq_lens, int B, int Hq, int Hkv, int C, int d,
+                             int t_new, float scale, void *workspace, size_t workspace_bytes,
+                             int32_t *dev_status, gqa_stream_t stream) {
+  const Operands op{q, k_cache, v_cache, nullptr, nullptr, nullptr, seq_lens, o, weights};
+  return rows_impl(dtype, op, false, B, Hq, Hkv, C, d, t_new, GQA_NO_WINDOW, scale, workspace,
+                   workspace_bytes, dev_status, stream);
+}
+
+}  // extern "C"

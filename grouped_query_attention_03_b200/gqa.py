@@ -23,15 +23,19 @@ STATUS_NAMES = {
     4: "GQA_ERR_WINDOW", 5: "GQA_ERR_CAPACITY", 6: "GQA_ERR_OVERFLOW",
     7: "GQA_ERR_UNSUPPORTED", 8: "GQA_ERR_WORKSPACE", 9: "GQA_ERR_CUDA",
     10: "GQA_ERR_DEVICE", 11: "GQA_ERR_TIMEOUT", 12: "GQA_ERR_SEGMENT",
+    13: "GQA_ERR_TREE",
 }
 
 # Every symbol include/gqa.h declares.
 EXPORTS = ("gqa_prefill", "gqa_prefill_packed", "gqa_decode", "gqa_decode_workspace_bytes",
            "gqa_decode_append", "gqa_decode_multi", "gqa_decode_noalloc", "gqa_cache_append", "gqa_cache_bytes",
            "gqa_ring_append", "gqa_ring_decode_append", "gqa_kv_head_for_query", "gqa_window_start", "gqa_prefill_kernel", "gqa_status_string",
-           "gqa_version", "gqa_selftest_wait_timeout")
+           "gqa_version", "gqa_selftest_wait_timeout", "gqa_qk_norm_rope", "gqa_decode_tree",
+           "gqa_decode_tree_workspace_bytes", "gqa_tree_commit", "gqa_decode_scored",
+           "gqa_decode_scored_workspace_bytes", "gqa_cache_evict")
 
 NOALLOC_SCRATCH_BYTES = 8 << 20  # GQA_NOALLOC_SCRATCH_BYTES in include/gqa.h
+MAX_TREE = 128  # GQA_MAX_TREE in include/gqa.h
 
 
 class GQAError(RuntimeError):
@@ -93,6 +97,20 @@ def _declare(L):
     L.gqa_version.restype = ctypes.c_char_p
     L.gqa_selftest_wait_timeout.argtypes = [i64, i32, vp, vp, vp]
     L.gqa_selftest_wait_timeout.restype = i32
+    L.gqa_qk_norm_rope.argtypes = [i32, vp, i64, i64, vp, vp, f32, vp, i32, i32, vp, i32,
+                                   vp, vp, vp, vp] + [i32] * 5 + [vp]
+    L.gqa_qk_norm_rope.restype = i32
+    L.gqa_decode_tree.argtypes = [i32] + [vp] * 8 + [i32] * 7 + [f32, vp, sz, vp, vp]
+    L.gqa_decode_tree.restype = i32
+    L.gqa_tree_commit.argtypes = [i32] + [vp] * 8 + [i32] * 6 + [vp, vp]
+    L.gqa_tree_commit.restype = i32
+    L.gqa_decode_scored.argtypes = [i32] + [vp] * 6 + [i32] * 6 + [f32, vp, sz, vp, vp]
+    L.gqa_decode_scored.restype = i32
+    for f in (L.gqa_decode_tree_workspace_bytes, L.gqa_decode_scored_workspace_bytes):
+        f.argtypes = [i32] * 7
+        f.restype = sz
+    L.gqa_cache_evict.argtypes = [i32] + [vp] * 9 + [i32] * 7 + [vp, vp]
+    L.gqa_cache_evict.restype = i32
     return L
 
 
@@ -143,6 +161,11 @@ def _ptr(t, name, dtype=None, device=None):
 def _stream(stream, device):
     s = stream if stream is not None else torch.cuda.current_stream(device)
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _check_lens(lens, B):
+    if lens.dim() != 1 or lens.shape[0] != B:
+        raise ValueError(f"lengths must be [{B}]")
 
 
 def _window(window):
@@ -380,6 +403,211 @@ def cache_append(k_cache, v_cache, k_new, v_new, seq_lens, *, status=None, strea
          _ptr(seq_lens, "seq_lens", torch.int32, dev), B, Hkv, C, d, t_new,
          _ptr(st, "status", torch.int32, dev), _stream(stream, dev))
     return st
+
+
+def qk_norm_rope(qkv, Hq, Hkv, d, *, q_weight=None, k_weight=None, eps=1e-6, inv_freq=None,
+                 interleaved=False, positions=None, axes=None, out=None, stream=None):
+    """The rows of one QKV projection, qkv [B,T,>=(Hq+2*Hkv)*d] (rows may be
+    strided), as normalised, position-rotated q [B,Hq,T,d], k and v
+    [B,Hkv,T,d].  q_weight/k_weight [d]: RMS norm of each query (key) head;
+    inv_freq [rot/2] float32: rotation of the first rot elements, pairs
+    (i, i + rot/2) or (interleaved) (2i, 2i + 1); positions int32 [B,T] or
+    [A,B,T] (None: 0..T-1), axes: the axis of each pair (a list of rot/2
+    numbers below A; None: all 0)."""
+    if qkv.dim() != 3 or (qkv.shape[2] > 1 and qkv.stride(2) != 1):
+        raise ValueError("qkv must be [B,T,width] with contiguous rows")
+    B, T, width = qkv.shape
+    if width < (Hq + 2 * Hkv) * d:
+        raise ValueError(f"qkv rows of {width} elements do not hold {Hq} + 2 * {Hkv} heads of {d}")
+    dev, dt = qkv.device, qkv.dtype
+    half = 0 if inv_freq is None else inv_freq.numel()
+    if positions is None:
+        naxes = 1
+    else:
+        if tuple(positions.shape[-2:]) != (B, T) or positions.dim() not in (2, 3):
+            raise ValueError("positions must be [B,T] or [axes,B,T]")
+        naxes = positions.shape[0] if positions.dim() == 3 else 1
+    pair_axis = None
+    if axes is not None:
+        if len(axes) != half:
+            raise ValueError(f"axes must name the axis of each of the {half} pairs")
+        pair_axis = (ctypes.c_int32 * half)(*axes)
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and w.numel() != d:
+            raise ValueError(f"{name} must have {d} elements")
+    if out is None:
+        out = tuple(torch.empty((B, h, T, d), dtype=dt, device=dev) for h in (Hq, Hkv, Hkv))
+    q, k, v = out
+    if q.shape != (B, Hq, T, d) or k.shape != (B, Hkv, T, d) or v.shape != k.shape:
+        raise ValueError("out must be q [B,Hq,T,d], k and v [B,Hkv,T,d]")
+    if not qkv.is_cuda:
+        raise ValueError("qkv must live in CUDA device memory")
+    # a dimension of one row has no meaningful stride
+    row_stride = qkv.stride(1) if T > 1 else width
+    batch_stride = qkv.stride(0) if B > 1 else 0
+    _run(dev, "gqa_qk_norm_rope", lib().gqa_qk_norm_rope,
+         _dtype_code(qkv), qkv.data_ptr(), batch_stride, row_stride,
+         _ptr(q_weight, "q_weight", dt, dev), _ptr(k_weight, "k_weight", dt, dev), float(eps),
+         _ptr(inv_freq, "inv_freq", torch.float32, dev), 2 * half, 1 if interleaved else 0,
+         _ptr(positions, "positions", torch.int32, dev), naxes, pair_axis,
+         _ptr(q, "q", dt, dev), _ptr(k, "k", dt, dev), _ptr(v, "v", dt, dev),
+         B, Hq, Hkv, T, d, _stream(stream, dev))
+    return q, k, v
+
+
+def decode_tree_workspace(q, k_cache):
+    """A device workspace for decode_tree on these shapes (no initial value;
+    reusable by later calls of any shape that fits)."""
+    B, Hq, t, d = q.shape
+    code = _dtype_code(q)
+    n = lib().gqa_decode_tree_workspace_bytes(code, B, Hq, k_cache.shape[1], k_cache.shape[2], d, t)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+
+
+def decode_tree(q, k_cache, v_cache, k_draft, v_draft, parents, seq_lens, *, window=None,
+                scale=None, out=None, workspace=None, status=None, stream=None):
+    """Attention for a tree of drafted tokens: q [B,Hq,t,d] the nodes'
+    queries, caches [B,Hkv,C,d] of seq_lens [B] int32 committed cells,
+    k_draft/v_draft [B,Hkv,t,d] the nodes' rows (not in the cache yet).  Node
+    i reads the committed cells and its own line in the tree; parents [B,t]
+    int32: -1 a root, -2 padding, None a chain."""
+    B, Hq, t, d = q.shape
+    Hkv, C = k_cache.shape[1], k_cache.shape[2]
+    if k_cache.shape != (B, Hkv, C, d) or v_cache.shape != k_cache.shape:
+        raise ValueError("cache shape mismatch")
+    if k_draft.shape != (B, Hkv, t, d) or v_draft.shape != k_draft.shape:
+        raise ValueError("drafted K/V must be [B,Hkv,t,d]")
+    if parents is not None and parents.shape != (B, t):
+        raise ValueError("parents must be [B, t]")
+    _check_lens(seq_lens, B)
+    if scale is None:
+        scale = d ** -0.5
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    elif out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    dev, dt = q.device, q.dtype
+    if workspace is None:
+        workspace = decode_tree_workspace(q, k_cache)
+    st = new_status(dev) if status is None else status
+    _run(dev, "gqa_decode_tree", lib().gqa_decode_tree,
+         _dtype_code(q), _ptr(q, "q"), _ptr(k_cache, "k_cache", dt, dev),
+         _ptr(v_cache, "v_cache", dt, dev), _ptr(k_draft, "k_draft", dt, dev),
+         _ptr(v_draft, "v_draft", dt, dev), _ptr(parents, "parents", torch.int32, dev),
+         _ptr(out, "out", dt, dev), _ptr(seq_lens, "seq_lens", torch.int32, dev),
+         B, Hq, Hkv, C, d, t, _window(window), float(scale),
+         _ptr(workspace, "workspace", torch.uint8, dev), workspace.numel(),
+         _ptr(st, "status", torch.int32, dev), _stream(stream, dev))
+    return out
+
+
+def tree_commit(k_cache, v_cache, k_draft, v_draft, path, path_lens, seq_lens, *, lens_out=None,
+                status=None, stream=None):
+    """The accepted path enters the cache: rows path[b, :path_lens[b]] (int32
+    [B,P], ascending nodes) of k_draft/v_draft [B,Hkv,t,d] go to cells
+    seq_lens[b] on, and lens_out (default: seq_lens itself) becomes seq_lens
+    + path_lens (all-or-nothing on the device).  Returns the status word."""
+    B, Hkv, C, d = k_cache.shape
+    t = k_draft.shape[2]
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("cache shape mismatch")
+    if k_draft.shape != (B, Hkv, t, d) or v_draft.shape != k_draft.shape:
+        raise ValueError("drafted K/V must be [B,Hkv,t,d]")
+    if path.dim() != 2 or path.shape[0] != B or path_lens.shape != (B,):
+        raise ValueError("path must be [B,P] and path_lens [B]")
+    _check_lens(seq_lens, B)
+    if lens_out is None:
+        lens_out = seq_lens
+    _check_lens(lens_out, B)
+    dev, dt = k_cache.device, k_cache.dtype
+    st = new_status(dev) if status is None else status
+    _run(dev, "gqa_tree_commit", lib().gqa_tree_commit,
+         _dtype_code(k_cache), _ptr(k_cache, "k_cache"), _ptr(v_cache, "v_cache", dt, dev),
+         _ptr(k_draft, "k_draft", dt, dev), _ptr(v_draft, "v_draft", dt, dev),
+         _ptr(path, "path", torch.int32, dev), _ptr(path_lens, "path_lens", torch.int32, dev),
+         _ptr(seq_lens, "seq_lens", torch.int32, dev), _ptr(lens_out, "lens_out", torch.int32, dev),
+         B, Hkv, C, d, t, path.shape[1], _ptr(st, "status", torch.int32, dev), _stream(stream, dev))
+    return st
+
+
+def decode_scored_workspace(q, k_cache):
+    """A device workspace for decode_scored on these shapes (no initial
+    value; reusable by later calls of any shape that fits)."""
+    B, Hq, t, d = q.shape if q.dim() == 4 else (*q.shape[:2], 1, q.shape[2])
+    code = _dtype_code(q)
+    n = lib().gqa_decode_scored_workspace_bytes(code, B, Hq, k_cache.shape[1], k_cache.shape[2], d, t)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+
+
+def decode_scored(q, k_cache, v_cache, weights, seq_lens, *, scale=None, out=None, workspace=None,
+                  status=None, stream=None):
+    """decode() (q [B,Hq,d]) or decode_multi() (q [B,Hq,t,d]) that also adds
+    to weights [B,Hkv,C] float32 the softmax weights each cell received."""
+    t = q.shape[2] if q.dim() == 4 else 1
+    B, Hq, d = q.shape[0], q.shape[1], q.shape[-1]
+    Hkv, C = k_cache.shape[1], k_cache.shape[2]
+    if k_cache.shape != (B, Hkv, C, d) or v_cache.shape != k_cache.shape:
+        raise ValueError("cache shape mismatch")
+    if weights.shape != (B, Hkv, C):
+        raise ValueError("weights must be [B,Hkv,C]")
+    _check_lens(seq_lens, B)
+    if scale is None:
+        scale = d ** -0.5
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    elif out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    dev, dt = q.device, q.dtype
+    if workspace is None:
+        workspace = decode_scored_workspace(q, k_cache)
+    st = new_status(dev) if status is None else status
+    _run(dev, "gqa_decode_scored", lib().gqa_decode_scored,
+         _dtype_code(q), _ptr(q, "q"), _ptr(k_cache, "k_cache", dt, dev),
+         _ptr(v_cache, "v_cache", dt, dev), _ptr(out, "out", dt, dev),
+         _ptr(weights, "weights", torch.float32, dev), _ptr(seq_lens, "seq_lens", torch.int32, dev),
+         B, Hq, Hkv, C, d, t, float(scale), _ptr(workspace, "workspace", torch.uint8, dev),
+         workspace.numel(), _ptr(st, "status", torch.int32, dev), _stream(stream, dev))
+    return out
+
+
+def cache_evict(k_cache, v_cache, weights, seq_lens, budget, recent, *, k_out=None, v_out=None,
+                weights_out=None, lens_out=None, kept=None, status=None, stream=None):
+    """Lanes of more than `budget` cells keep their last `recent` and, of the
+    others, the budget - recent with the largest weights [B,Hkv,C] float32,
+    in their order: in place, or into k_out/v_out [B,Hkv,C_out,d] and
+    weights_out [B,Hkv,C_out].  lens_out (default: seq_lens itself) becomes
+    min(seq_lens, budget).  Returns kept [B,Hkv,budget] int32, the cell that
+    each kept row came from (-1 behind them)."""
+    B, Hkv, C, d = k_cache.shape
+    if v_cache.shape != k_cache.shape or weights.shape != (B, Hkv, C):
+        raise ValueError("cache and weights shape mismatch")
+    if k_out is None and v_out is None and weights_out is None:
+        k_out, v_out, weights_out = k_cache, v_cache, weights
+    elif k_out is None or v_out is None or weights_out is None:
+        raise ValueError("k_out, v_out and weights_out come together")
+    C_out = k_out.shape[2]
+    if k_out.shape != (B, Hkv, C_out, d) or v_out.shape != k_out.shape or \
+            weights_out.shape != (B, Hkv, C_out):
+        raise ValueError("output shape mismatch")
+    _check_lens(seq_lens, B)
+    if lens_out is None:
+        lens_out = seq_lens
+    _check_lens(lens_out, B)
+    dev, dt = k_cache.device, k_cache.dtype
+    if kept is None:
+        kept = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=dev)
+    elif kept.shape != (B, Hkv, budget):
+        raise ValueError("kept must be [B,Hkv,budget]")
+    st = new_status(dev) if status is None else status
+    _run(dev, "gqa_cache_evict", lib().gqa_cache_evict,
+         _dtype_code(k_cache), _ptr(k_cache, "k_cache"), _ptr(v_cache, "v_cache", dt, dev),
+         _ptr(weights, "weights", torch.float32, dev), _ptr(seq_lens, "seq_lens", torch.int32, dev),
+         _ptr(k_out, "k_out", dt, dev), _ptr(v_out, "v_out", dt, dev),
+         _ptr(weights_out, "weights_out", torch.float32, dev),
+         _ptr(lens_out, "lens_out", torch.int32, dev), _ptr(kept, "kept", torch.int32, dev),
+         B, Hkv, C, C_out, d, int(budget), int(recent), _ptr(st, "status", torch.int32, dev),
+         _stream(stream, dev))
+    return kept
 
 
 def cache_bytes(L, B, T, Hkv, d, elem_bytes):

@@ -70,8 +70,11 @@ typedef enum {
   GQA_ERR_DEVICE = 10,     /* the current device is not sm_100 */
   GQA_ERR_TIMEOUT = 11,    /* a kernel's bounded internal wait ran out (set
                               in *dev_status only) */
-  GQA_ERR_SEGMENT = 12     /* a packed segment start s_{b,t} lies outside
+  GQA_ERR_SEGMENT = 12,    /* a packed segment start s_{b,t} lies outside
                               [0, t] (set in *dev_status only) */
+  GQA_ERR_TREE = 13        /* a drafted token's parent is not an earlier
+                              live one, or an accepted path is not ascending
+                              inside the tree (set in *dev_status only) */
 } gqa_status;
 
 #define GQA_NO_WINDOW (-1)
@@ -315,6 +318,160 @@ gqa_status gqa_cache_append(gqa_dtype dtype, void *k_cache, void *v_cache,
                             int32_t *seq_lens, int B, int Hkv, int C, int d,
                             int t_new, int32_t *dev_status,
                             gqa_stream_t stream);
+
+/*
+ * gqa_qk_norm_rope -- the step before the attention: the rows of one QKV
+ * projection become normalised, position-rotated queries and keys, and the
+ * values, in the layouts that the attention entry points take ([P1] "Give
+ * each query head an explicit shared KV head" rotates q and k before the
+ * scores and caches rotated keys).
+ *
+ *   qkv      [B,T,(Hq + 2 Hkv) d]: query heads, key heads, value heads.  Rows
+ *            may be apart: element (b, t, 0) is at b * batch_stride + t *
+ *            row_stride (in elements, row_stride >= (Hq + 2 Hkv) d)
+ *   q_weight, k_weight  [d] of the same type, or NULL: a query (key) head's
+ *            row x becomes x / sqrt(mean(x^2) + eps) * weight; NULL leaves it
+ *   inv_freq device float [rot_d / 2]: finite frequencies in radians per
+ *            position; NULL only when rot_d = 0 (no rotation)
+ *   rot_d    rotated elements of a head, even, <= d; the rest pass
+ *   interleaved  0: pair i is elements (i, i + rot_d / 2); else (2i, 2i + 1).
+ *            (u, v) becomes (u cos a - v sin a, v cos a + u sin a)
+ *   positions  device int32 [axes,B,T], any value, or NULL: position t (one
+ *            axis).  a = positions[axis of pair i][b,t] * inv_freq[i], exact
+ *            to fp32 at every position
+ *   axes     1 .. 4 position axes (text: 1; images and video: time, height,
+ *            width)
+ *   pair_axis  HOST int32 [rot_d / 2], each in [0, axes), read during the
+ *            call; NULL: all 0
+ *   q        [B,Hq,T,d], k, v [B,Hkv,T,d]: outputs, not overlapping qkv.
+ *            With T = 1 they are gqa_decode_append's q, k_new, v_new
+ * fp32 arithmetic, one rounding.  16-byte-aligned buffers, widths and strides
+ * (and halves rot_d / 2) run the vector kernel, others a row kernel.
+ */
+gqa_status gqa_qk_norm_rope(gqa_dtype dtype, const void *qkv, int64_t batch_stride,
+                            int64_t row_stride, const void *q_weight, const void *k_weight,
+                            float eps, const float *inv_freq, int rot_d, int interleaved,
+                            const int32_t *positions, int axes, const int32_t *pair_axis,
+                            void *q, void *k, void *v, int B, int Hq, int Hkv, int T, int d,
+                            gqa_stream_t stream);
+
+/* Most drafted tokens (or scored rows) per sequence. */
+#define GQA_MAX_TREE 128
+
+/*
+ * gqa_decode_tree -- attention for a tree of drafted tokens over a cache.
+ * [P1] "Extend the existing full and cached attention paths": candidate rows
+ * take part in the scores before they are committed to the cache; here the
+ * candidates are a tree, and node i reads the committed cells and its own
+ * ancestors (itself included), nothing else.
+ *
+ *   q        [B,Hq,t_new,d]   the nodes' queries (rotated; a node's position
+ *            is seq_lens[b] + its depth, a root's depth being 0)
+ *   k_cache, v_cache [B,Hkv,C,d]; seq_lens device int32 [B]: committed cells,
+ *            in [0, C].  Neither is changed, and the cache needs no room
+ *   k_draft, v_draft [B,Hkv,t_new,d]  the nodes' keys (rotated) and values
+ *   parents  device int32 [B,t_new]: node i's parent, -1 (a root; several
+ *            are allowed) or a live earlier node; -2: padding, no node (its
+ *            output is zero and its rows are not used).  NULL: a chain,
+ *            parent i - 1
+ *   o        [B,Hq,t_new,d]
+ *   window   as elsewhere, counted in positions: a node at depth m reads
+ *            cells >= seq_lens[b] + m - (w - 1) and its last w - 1 ancestors
+ *   workspace  gqa_decode_tree_workspace_bytes(...) bytes, 256-byte aligned;
+ *            needs no initial value and keeps none.  Calls sharing it must
+ *            be ordered
+ *   dev_status device int32 (required)
+ * A length outside [0, C] sets GQA_ERR_CAPACITY and zeroes that sequence's
+ * output.  A parent outside [-2, i), or one that is padding or itself
+ * refused, sets GQA_ERR_TREE and zeroes that node's output.  t_new >
+ * GQA_MAX_TREE returns GQA_ERR_UNSUPPORTED.  What a node may not read never
+ * reaches its output, whatever it holds.  bf16 with d in {64, 128} runs a
+ * split-K tcgen05 kernel; other d and fp32 run CUDA cores, split likewise.
+ */
+gqa_status gqa_decode_tree(gqa_dtype dtype, const void *q, const void *k_cache,
+                           const void *v_cache, const void *k_draft, const void *v_draft,
+                           const int32_t *parents, void *o, const int32_t *seq_lens, int B,
+                           int Hq, int Hkv, int C, int d, int t_new, int window, float scale,
+                           void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                           gqa_stream_t stream);
+
+/* Workspace gqa_decode_tree needs for these sizes; 0
+ * for invalid sizes, which gqa_decode_tree then rejects. */
+size_t gqa_decode_tree_workspace_bytes(gqa_dtype dtype, int B, int Hq, int Hkv, int C, int d,
+                                       int t_new);
+
+/*
+ * gqa_tree_commit -- the accepted path of a drafted tree enters the cache
+ * (gqa_cache_append of selected rows): row path[b][j] of k_draft / v_draft
+ * goes to cell seq_lens[b] + j for j < path_lens[b], and lens_out[b] =
+ * seq_lens[b] + path_lens[b].
+ *
+ *   path     device int32 [B,max_path]: strictly ascending nodes in [0,
+ *            t_new); entries from path_lens[b] on are not read
+ *   path_lens device int32 [B], in [0, min(max_path, t_new)]
+ *   lens_out device int32 [B]; may be seq_lens itself
+ * All-or-nothing over the batch: a sequence that would pass C sets
+ * GQA_ERR_CAPACITY, an invalid path GQA_ERR_TREE, and then no cell changes
+ * and lens_out receives seq_lens.
+ */
+gqa_status gqa_tree_commit(gqa_dtype dtype, void *k_cache, void *v_cache, const void *k_draft,
+                           const void *v_draft, const int32_t *path, const int32_t *path_lens,
+                           const int32_t *seq_lens, int32_t *lens_out, int B, int Hkv, int C,
+                           int d, int t_new, int max_path, int32_t *dev_status,
+                           gqa_stream_t stream);
+
+/*
+ * gqa_decode_scored -- gqa_decode_multi (t_new = 1: gqa_decode) without a
+ * window that also keeps account of how much each cell was looked at:
+ * weights[b,g,j] += the softmax weights that cell j of KV head g receives
+ * from the t_new rows of the group's query heads.
+ *
+ *   q        [B,Hq,t_new,d]; row i sits at cell n_b - t_new + i
+ *   weights  device float [B,Hkv,C], in/out; cells >= n_b are left alone
+ *   seq_lens device int32 [B], n_b in [t_new, C]
+ *   workspace  gqa_decode_scored_workspace_bytes(...) bytes, 256-byte
+ *            aligned, no initial value (it holds the scores: 4 bytes per
+ *            query row and cell); calls sharing it must be ordered
+ * A length outside [t_new, C] sets GQA_ERR_CAPACITY, zeroes that sequence's
+ * output and leaves its weights.  t_new > GQA_MAX_TREE returns
+ * GQA_ERR_UNSUPPORTED.
+ */
+gqa_status gqa_decode_scored(gqa_dtype dtype, const void *q, const void *k_cache,
+                             const void *v_cache, void *o, float *weights,
+                             const int32_t *seq_lens, int B, int Hq, int Hkv, int C, int d,
+                             int t_new, float scale, void *workspace, size_t workspace_bytes,
+                             int32_t *dev_status, gqa_stream_t stream);
+
+/* Workspace gqa_decode_scored needs for these sizes; 0
+ * for invalid sizes, which gqa_decode_scored then rejects. */
+size_t gqa_decode_scored_workspace_bytes(gqa_dtype dtype, int B, int Hq, int Hkv, int C, int d,
+                                         int t_new);
+
+/*
+ * gqa_cache_evict -- the cells that were looked at least leave the cache.
+ * Per lane (b, g) with n_b > budget: the last `recent` cells stay, and of
+ * the others the budget - recent with the largest weights (equal weights:
+ * the lower cell first; NaN below everything).  The cells that stay move up
+ * in their order.  Rows are moved as they are: a key keeps the rotation of
+ * its own position, and from then on a cell's number is not its position.
+ *
+ *   weights  device float [B,Hkv,C]
+ *   k_out, v_out [B,Hkv,C_out,d], weights_out [B,Hkv,C_out]: other buffers
+ *            than the inputs, or all three the inputs themselves (in place,
+ *            C_out = C).  weights_out is zero from the new length on
+ *   lens_out device int32 [B]: min(n_b, budget); may be seq_lens itself
+ *   kept     device int32 [B,Hkv,budget]: the cell that each kept row came
+ *            from, then -1
+ *   budget <= C_out, recent <= budget (else GQA_ERR_CAPACITY)
+ * A length outside [0, C] sets GQA_ERR_CAPACITY; that sequence's rows,
+ * weights and length do not change (lens_out receives the length as it is)
+ * and its kept is -1.
+ */
+gqa_status gqa_cache_evict(gqa_dtype dtype, const void *k_cache, const void *v_cache,
+                           const float *weights, const int32_t *seq_lens, void *k_out,
+                           void *v_out, float *weights_out, int32_t *lens_out, int32_t *kept,
+                           int B, int Hkv, int C, int C_out, int d, int budget, int recent,
+                           int32_t *dev_status, gqa_stream_t stream);
 
 /* [P3] "Computing the cache requirement": 2*L*B*T*Hkv*d*e bytes for L
  * layers; 0 if any argument is negative or the product overflows uint64. */
