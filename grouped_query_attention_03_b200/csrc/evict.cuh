@@ -6,16 +6,19 @@
 // order.  Weights compare by value; -0 equals 0 and NaN is below everything.
 //
 // evict_select_kernel, one CTA per lane: the weights become ordered 32-bit
-// keys held in registers (KPT per thread; longer lanes read them again from
-// L2 every round).  The largest threshold T that at least k keys reach is
-// built from its top bits, two bits per round: each round counts the keys
-// that reach the three candidates, so 16 rounds of compares and one block
-// reduction find the k-th largest key exactly, whatever the distribution,
-// with no atomics (a histogram's would meet on the few bins that weights of
-// one magnitude share).  A round ends the search early when exactly k keys
-// reach its threshold.  One prefix sum over (above T, equal to T) places
-// every survivor; the CTA writes the list `kept` and its lane's weights
-// (read completely before, so they may be compacted in place).
+// keys, held in registers up to 32 per thread (longer lanes read them again
+// from L2).  The k-th largest key T is found digit by digit from the top, 12,
+// 10 and 10 bits: a histogram of the digit over the keys that share T's
+// higher digits, suffix sums over its bins, the bin that holds rank k.  What
+// bounds it is the SM's issue rate, 32768 keys being 1024 warp instructions
+// per step of the loop: three passes of one comparison and few additions
+// where a search by thresholds takes 16 passes of three comparisons each
+// (measured: 8 lanes of 32768 cells 55 us by thresholds of 2 bits).  A warp
+// whose lanes agree on a bin adds them at once, so equal weights (zeros, a
+// fresh cache) do not queue up on one counter.  A pass that finds exactly k
+// keys from T's bin up ends the search.  One prefix sum over (above T, equal
+// to T) places every survivor; the CTA writes the list `kept` and its lane's
+// weights (read completely before, so they may be compacted in place).
 //
 // Moving the rows (evict_move_kernel) is a gather through `kept`, bound by
 // bandwidth.  Into other caches any order will do: evict_copy_kernel.  In
@@ -55,24 +58,42 @@ __device__ __forceinline__ float key_weight(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
 }
 
-// Sums (a, b, c) over the block; every thread gets them.  `buf` alternates
-// between two halves so that one barrier per call is enough.
-__device__ __forceinline__ void block_sum3(uint32_t &a, uint32_t &b, uint32_t &c,
-                                           uint32_t (*buf)[3][kWarps], int &turn) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  a = __reduce_add_sync(0xffffffffu, a);
-  b = __reduce_add_sync(0xffffffffu, b);
-  c = __reduce_add_sync(0xffffffffu, c);
-  if (lane == 0) {
-    buf[turn][0][warp] = a;
-    buf[turn][1][warp] = b;
-    buf[turn][2][warp] = c;
+constexpr int kBins = 4096;  // of the first, 12-bit digit
+
+// Finds rank k (from the top, 1-based, at most the total count) among the
+// bins: the bin that holds it, the count above that bin, its own count.
+// Block-wide; BINS is a multiple of kSelThreads.
+template <int BINS>
+__device__ __forceinline__ void find_bin(const uint32_t *hist, uint32_t k, uint32_t *warp_sum,
+                                         uint32_t *result) {
+  constexpr int PER = BINS / kSelThreads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // thread t has bins [BINS - (t + 1) PER, BINS - t PER), from the top down
+  uint32_t c[PER], sum = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    c[i] = hist[BINS - 1 - tid * PER - i];
+    sum += c[i];
+  }
+  uint32_t incl = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += y;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  uint32_t above = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0u);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (above < k && k <= above + c[i]) {  // one thread, one bin
+      result[0] = BINS - 1 - tid * PER - i;
+      result[1] = above;
+      result[2] = c[i];
+    }
+    above += c[i];
   }
   __syncthreads();
-  a = __reduce_add_sync(0xffffffffu, buf[turn][0][lane]);
-  b = __reduce_add_sync(0xffffffffu, buf[turn][1][lane]);
-  c = __reduce_add_sync(0xffffffffu, buf[turn][2][lane]);
-  turn ^= 1;
 }
 
 // KPT > 0: lanes of at most KPT * kSelThreads cells, keys in registers;
@@ -80,9 +101,10 @@ __device__ __forceinline__ void block_sum3(uint32_t &a, uint32_t &b, uint32_t &c
 template <int KPT>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params p) {
   constexpr int STRIPS = KPT > 0 ? KPT : 8;  // strips of kSelThreads cells placed at a time
-  __shared__ uint32_t sums[2][3][kWarps];
-  __shared__ uint32_t place[STRIPS * kWarps][2];
-  __shared__ uint32_t wsum[kWarps][2];
+  __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t found[3];
+  __shared__ uint32_t place[STRIPS * kWarps][2], masks[STRIPS * kWarps][2];
+  __shared__ uint32_t wsum[kWarps][2], wtop[kWarps];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -114,46 +136,50 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params 
       key[i] = j < n ? order_key(w[j]) : 0u;
     }
   }
-  // T: the k-th largest candidate key; `more` candidates are above T - or,
-  // after an early end, T is any threshold that exactly k reach
+  // T: the k-th largest candidate key, or after an early end the lower bound
+  // of its bin
   uint32_t T = 0, need = 0;  // need: how many of the keys equal to T stay
   bool exact = false;        // every key >= T stays
-  int turn = 0;
   if (k > 0) {
-    for (int bit = 30; bit >= 0 && !exact; bit -= 2) {
-      const uint32_t t1 = T | (1u << bit), t2 = T | (2u << bit), t3 = T | (3u << bit);
-      uint32_t c1 = 0, c2 = 0, c3 = 0;
+    uint32_t rank = k;  // of T among the keys that share its higher digits
+#pragma unroll
+    for (int pass = 0; pass < 3 && !exact; ++pass) {
+      const int shift = pass == 0 ? 20 : (pass == 1 ? 10 : 0);
+      const uint32_t low = pass == 0 ? 4095u : 1023u;
+      const int upper = shift + (pass == 0 ? 12 : 10);  // bits above the digit are T's
+      for (int i = tid; i < (int)low + 1; i += kSelThreads) hist[i] = 0;
+      __syncthreads();
       auto count = [&](int j, uint32_t x) {
-        if (j < nc) {
-          c1 += x >= t1;
-          c2 += x >= t2;
-          c3 += x >= t3;
-        }
+        const bool in = j < nc && (pass == 0 || (x >> (upper & 31)) == (T >> (upper & 31)));
+        const uint32_t bin = (x >> shift) & low;
+        const unsigned some = __ballot_sync(0xffffffffu, in);
+        if (some == 0) return;
+        // the lanes that agree with the first counted one go together
+        const int first = __ffs(some) - 1;
+        const uint32_t b0 = __shfl_sync(0xffffffffu, bin, first);
+        const unsigned same = __ballot_sync(0xffffffffu, in && bin == b0);
+        if (lane == first) atomicAdd(&hist[b0], __popc(same));
+        if (in && bin != b0) atomicAdd(&hist[bin], 1u);
       };
       if constexpr (KPT > 0) {
 #pragma unroll
         for (int i = 0; i < KPT; ++i) count(i * kSelThreads + tid, key[i]);
       } else {
-        for (int j = tid; j < nc; j += kSelThreads) count(j, order_key(w[j]));
+        for (int j0 = 0; j0 < nc; j0 += kSelThreads) {
+          const int j = j0 + tid;
+          count(j, j < nc ? order_key(w[j]) : 0u);
+        }
       }
-      block_sum3(c1, c2, c3, sums, turn);
-      uint32_t c = 0;
-      if (c3 >= k) { T = t3; c = c3; }
-      else if (c2 >= k) { T = t2; c = c2; }
-      else if (c1 >= k) { T = t1; c = c1; }
-      exact = c == k;
+      __syncthreads();
+      if (pass == 0)
+        find_bin<4096>(hist, rank, wtop, found);
+      else
+        find_bin<1024>(hist, rank, wtop, found);
+      T |= found[0] << shift;
+      rank -= found[1];
+      exact = rank == found[2];
     }
-    if (!exact) {
-      uint32_t above = 0, z0 = 0, z1 = 0;
-      if constexpr (KPT > 0) {
-#pragma unroll
-        for (int i = 0; i < KPT; ++i) above += (i * kSelThreads + tid < nc) && key[i] > T;
-      } else {
-        for (int j = tid; j < nc; j += kSelThreads) above += order_key(w[j]) > T;
-      }
-      block_sum3(above, z0, z1, sums, turn);
-      need = k - above;
-    }
+    need = rank;  // used when not exact: T is then a key, `rank` of its equals stay
   }
   // Place the survivors, STRIPS * kSelThreads cells at a time in ascending
   // order: cell -> strip, warp, lane.
@@ -179,6 +205,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params 
       if (lane == 0) {
         place[i * kWarps + warp][0] = __popc(ms);
         place[i * kWarps + warp][1] = __popc(me);
+        masks[i * kWarps + warp][0] = ms;
+        masks[i * kWarps + warp][1] = me;
       }
     }
     __syncthreads();
@@ -218,9 +246,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params 
 #pragma unroll
     for (int i = 0; i < STRIPS; ++i) {
       const int j = s0 + i * kSelThreads + tid;
-      const bool sure = sure_of(j, key[i]), eq = equal_of(j, key[i]);
-      const uint32_t ms = __ballot_sync(0xffffffffu, sure);
-      const uint32_t me = __ballot_sync(0xffffffffu, eq);
+      const uint32_t ms = masks[i * kWarps + warp][0], me = masks[i * kWarps + warp][1];
+      const bool sure = (ms >> lane) & 1, eq = (me >> lane) & 1;
       const uint32_t s = place[i * kWarps + warp][0] + __popc(ms & below);
       const uint32_t e = place[i * kWarps + warp][1] + __popc(me & below);
       if (sure || (eq && e < need)) {

@@ -5,6 +5,7 @@
 #include "host.cuh"
 #include "rows_simt.cuh"
 #include "rows_splitk.cuh"
+#include "rows_weigh_tc.cuh"
 
 namespace {
 
@@ -17,11 +18,30 @@ using gqa::rows::Params;
 constexpr int kMaxCtas = 256;
 constexpr int kSimtCtas = 592;
 
+// Tiles a CTA takes at least, and what a lane group costs it in tiles.
+#ifndef GQA_ROWS_MIN_TILES
+#define GQA_ROWS_MIN_TILES 1
+#endif
+#ifndef GQA_ROWS_PAD
+#define GQA_ROWS_PAD 3
+#endif
+constexpr int kMinTiles = GQA_ROWS_MIN_TILES;
+constexpr int kPadTiles = GQA_ROWS_PAD;
+
+// Rows times parts that the last CTA to count a lane group's parts merges
+// itself; more than that is shared by all SMs in a kernel of its own.
+#ifndef GQA_ROWS_MERGE
+#define GQA_ROWS_MERGE 800
+#endif
+constexpr int kMergeRows = GQA_ROWS_MERGE;
+
 struct Layout {
   bool tc = false;
+  bool finish = false;  // the parts are merged by a kernel of their own
+  bool scores = false;  // scored: the scores are kept, not multiplied again
   int NT = 1, group_rows = 0, MG = 1, ns = 0, Cp = 0;
   int64_t slots = 0;
-  size_t ml = 0, acc = 0, scores = 0, total = 0;
+  size_t splits = 0, ml = 0, acc = 0, lse = 0, score_at = 0, total = 0;  // counters at 0
 };
 
 // Sizes only (no pointers): what gqa_decode_*_workspace_bytes can know.  The
@@ -41,6 +61,11 @@ bool layout(gqa_dtype dtype, int B, int Hq, int Hkv, int C, int d, int t, bool s
     L.MG = (int)((R + 2 * gqa::rows::kM - 1) / (2 * gqa::rows::kM));
     L.group_rows = L.MG == 1 ? (int)R : 2 * gqa::rows::kM;
     L.slots = lanes * L.MG + kMaxCtas;
+    // Parts per lane group if all sequences are of one length, times their
+    // rows: what the last CTA to count would have to read.
+    const int64_t parts = kMaxCtas / 2 / std::max<int64_t>(lanes * L.MG, 1) + 2;
+    L.finish = parts * L.group_rows > kMergeRows;
+    L.scores = scored && R <= d / 4;
   } else {
     L.group_rows = gqa::rows::kSR;
     L.MG = (int)((R + gqa::rows::kSR - 1) / gqa::rows::kSR);
@@ -50,18 +75,26 @@ bool layout(gqa_dtype dtype, int B, int Hq, int Hkv, int C, int d, int t, bool s
     L.ns = (int)std::min<int64_t>(std::min<int64_t>(most, 64),
                                   std::max<int64_t>(1, kSimtCtas / std::max<int64_t>(groups, 1)));
     L.slots = groups * L.ns;
+    L.scores = scored;
   }
   int64_t n;
-  if (!elems(&n, {L.slots, L.group_rows, 8}) || n > INT64_MAX / 4) return false;
-  L.acc = round256((size_t)n);
-  if (!elems(&n, {L.slots, L.group_rows, d, 4}) || n > INT64_MAX / 4) return false;
-  L.scores = L.acc + round256((size_t)n);
-  L.total = L.scores;
+  L.splits = round256(gqa::rows::kCounters * sizeof(int));
+  L.ml = L.splits + round256(kMaxCtas * sizeof(int2));
+  if (!elems(&n, {L.slots, L.group_rows, 8}) || n > INT64_MAX / 8) return false;
+  L.acc = L.ml + round256((size_t)n);
+  if (!elems(&n, {L.slots, L.group_rows, (d + 3) / 4, 16}) || n > INT64_MAX / 8) return false;
+  L.lse = L.acc + round256((size_t)n);
+  L.total = L.lse;
   if (scored) {
+    if (!elems(&x, {lanes, R, 8}) || x > INT64_MAX / 8) return false;
+    L.score_at = L.lse + round256((size_t)x);
+    L.total = L.score_at;
     if (C > INT_MAX - gqa::rows::kTile) return false;
     L.Cp = (C + gqa::rows::kTile - 1) / gqa::rows::kTile * gqa::rows::kTile;
-    if (!elems(&x, {lanes, R, L.Cp, 4}) || x > INT64_MAX / 4) return false;
-    L.total += round256((size_t)x);
+    if (L.scores) {
+      if (!elems(&x, {lanes, R, L.Cp, 4}) || x > INT64_MAX / 8) return false;
+      L.total += round256((size_t)x);
+    }
   }
   *out = L;
   return true;
@@ -71,9 +104,9 @@ template <int D, int NT>
 gqa_status launch_tc(const Params &p, const DeviceInfo &di, cudaStream_t st) {
   using K = gqa::rows::TcCfg<D, NT>;
   CUtensorMap mq, mk, mv, mkd, mvd;
-  const long long qrows = (long long)p.B * p.Hq * p.t;
   const int lanes = p.B * p.Hkv;
-  if (!gqa::tma::make_bf16_map(&mq, p.q, D, qrows, 0, 128)) return GQA_ERR_CUDA;
+  // a lane's rows are consecutive; those past them read as zeros
+  if (!gqa::tma::make_bf16_map(&mq, p.q, D, p.R, lanes, 128)) return GQA_ERR_CUDA;
   if (p.C > 0 && (!gqa::tma::make_bf16_map(&mk, p.k, D, p.C, lanes, 128) ||
                   !gqa::tma::make_bf16_map(&mv, p.v, D, p.C, lanes, 128)))
     return GQA_ERR_CUDA;
@@ -93,8 +126,23 @@ gqa_status launch_tc(const Params &p, const DeviceInfo &di, cudaStream_t st) {
   gqa_status s = allow_smem(gqa::rows::rows_splitk_kernel<D, NT>, K::SMEM, di.id, done);
   if (s != GQA_OK) return s;
   return launched(gqa::launch_dependent(gqa::rows::rows_splitk_kernel<D, NT>,
-                                        dim3((unsigned)p.ctas), dim3(K::THREADS), K::SMEM, st, mq,
+                                        dim3((unsigned)p.ctas), dim3(gqa::rows::kTcThreads), K::SMEM, st, mq,
                                         mk, mv, mkd, mvd, p));
+}
+
+template <int D>
+gqa_status launch_weigh_tc(const Params &p, const DeviceInfo &di, cudaStream_t st) {
+  using K = gqa::rows::WgCfg<D>;
+  CUtensorMap mq, mk;
+  if (!gqa::tma::make_bf16_map(&mq, p.q, D, p.R, p.B * p.Hkv, 128) ||
+      !gqa::tma::make_bf16_map(&mk, p.k, D, p.C, p.B * p.Hkv, 128))
+    return GQA_ERR_CUDA;
+  static bool done[64] = {};
+  gqa_status s = allow_smem(gqa::rows::rows_weigh_tc_kernel<D>, K::SMEM, di.id, done);
+  if (s != GQA_OK) return s;
+  return launched(gqa::launch_dependent(gqa::rows::rows_weigh_tc_kernel<D>,
+                                        dim3((unsigned)di.sms), dim3(gqa::rows::kTcThreads),
+                                        K::SMEM, st, mq, mk, p));
 }
 
 template <typename T>
@@ -157,9 +205,13 @@ gqa_status rows_impl(gqa_dtype dtype, const Operands &op, bool tree, int B, int 
   p.seq_lens = op.seq_lens;
   p.o = op.o;
   p.status = dev_status;
+  p.counters = reinterpret_cast<int *>(ws);
+  p.splits = reinterpret_cast<int2 *>(ws + L.splits);
+  p.finish = L.finish ? 1 : 0;
   p.ml = reinterpret_cast<float2 *>(ws + L.ml);
   p.acc = reinterpret_cast<float *>(ws + L.acc);
-  p.scores = tree ? nullptr : reinterpret_cast<float *>(ws + L.scores);
+  p.lse = tree ? nullptr : reinterpret_cast<float2 *>(ws + L.lse);
+  p.scores = L.scores ? reinterpret_cast<float *>(ws + L.score_at) : nullptr;
   p.weights = op.weights;
   p.B = B;
   p.Hq = Hq;
@@ -175,16 +227,13 @@ gqa_status rows_impl(gqa_dtype dtype, const Operands &op, bool tree, int B, int 
   p.group_rows = L.group_rows;
   p.MG = L.MG;
   p.ctas = std::min(kMaxCtas, di.sms);
-  p.min_tiles = 1;
+  p.min_tiles = kMinTiles;
+  p.pad = kPadTiles;
   p.ns = L.ns;
   p.scale_log2 = scale * gqa::kLog2e;
-  // the merge's grid, checked before anything is launched
-  const int64_t groups = (int64_t)B * Hkv * L.MG;
-  const int row_blocks = (std::min(L.group_rows, p.R) + 7) / 8;
-  const int cell_blocks = tree ? 0 : (C + gqa::rows::kFinishCells - 1) / gqa::rows::kFinishCells;
-  const bool merges = L.tc || L.ns > 1;
-  const int64_t merge_blocks = merges ? groups * row_blocks : 0;
-  const int64_t grid = merge_blocks + (int64_t)B * Hkv * cell_blocks;
+  // the weights' grid, checked before anything is launched
+  const int cell_blocks = (C + gqa::rows::kWeighCells - 1) / gqa::rows::kWeighCells;
+  const int64_t grid = tree ? 0 : (int64_t)B * Hkv * cell_blocks;
   if (grid > INT_MAX) return GQA_ERR_UNSUPPORTED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (L.tc) {
@@ -195,12 +244,19 @@ gqa_status rows_impl(gqa_dtype dtype, const Operands &op, bool tree, int B, int 
   } else {
     s = dtype == GQA_F32 ? launch_simt<float>(p, di, st) : launch_simt<__nv_bfloat16>(p, di, st);
   }
-  if (s != GQA_OK || grid == 0) return s;
-  auto *finish = dtype == GQA_F32 ? gqa::rows::rows_finish_kernel<float>
-                                  : gqa::rows::rows_finish_kernel<__nv_bfloat16>;
-  return launched(gqa::launch_dependent(finish, dim3((unsigned)grid),
-                                        dim3(gqa::rows::kFinishThreads), 0, st, p,
-                                        (int)merge_blocks, row_blocks, cell_blocks));
+  if (s != GQA_OK) return s;
+  if (L.finish) {
+    const int row_blocks = (std::min(L.group_rows, p.R) + gqa::rows::kFinishRows - 1) / gqa::rows::kFinishRows;
+    const int col_blocks = d / gqa::rows::kFinishCols;
+    s = launched(gqa::launch_dependent(gqa::rows::rows_finish_kernel<__nv_bfloat16>,
+                                       dim3((unsigned)(p.ctas * row_blocks * col_blocks)),
+                                       dim3(gqa::rows::kFinishThreads), 0, st, p, row_blocks, col_blocks));
+    if (s != GQA_OK) return s;
+  }
+  if (tree) return s;
+  if (!L.scores) return d == 64 ? launch_weigh_tc<64>(p, di, st) : launch_weigh_tc<128>(p, di, st);
+  return launched(gqa::launch_dependent(gqa::rows::rows_weigh_kernel, dim3((unsigned)grid),
+                                        dim3(gqa::rows::kWeighThreads), 0, st, p, cell_blocks));
 }
 
 // The larger of the two layouts: buffers that are not 16-byte aligned run

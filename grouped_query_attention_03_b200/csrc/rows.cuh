@@ -10,12 +10,16 @@
 //   scored  row i reads cells [0, n_b - t_new + i]
 // The keys are split over CTAs, each writes (m, l, acc) of its part - the
 // maximum of the scaled scores (log2 units), the sum of 2^(s - m), and the
-// mix of values - and rows_finish_kernel merges the parts in order:
+// mix of values - to the workspace, and the parts are merged in order:
 //   m = max m_i, l = sum 2^(m_i - m) l_i, o = sum 2^(m_i - m) acc_i / l.
-// scored: the parts also leave every scaled score s in the workspace, and
-// the same kernel adds sum_rho 2^(s - m_rho) / l_rho to the cell's weight.
-// The scores cost 8 bytes per row and cell (written, read) where reading the
-// keys again would cost 2 d: less up to r * t_new = 32 rows at d = 128.
+// Few small parts: by the last CTA to count a lane's parts (the counters are
+// zero between calls, the last count resets them).  Many or large ones: by
+// rows_finish_kernel, all SMs together (p.finish).  Either way the bits do
+// not depend on who merges, and no CTA waits for another.
+// scored: every row's m and 1 / l are kept, and a second kernel adds
+// sum_rho 2^(s - m_rho) / l_rho to each cell's weight: from the scores, left
+// in the workspace by the parts (rows_weigh_kernel), or from the keys, read
+// once more (rows_weigh_tc.cuh).
 #pragma once
 
 #include "common.cuh"
@@ -34,15 +38,20 @@ struct Params {
   void *o;
   int32_t *status;
   float2 *ml;               // [slot][group_rows]
-  float *acc;               // [slot][group_rows][d]
-  float *scores;            // [B * Hkv][R][Cp] (scored), else NULL
+  float *acc;               // [slot][ceil(d / 4)][group_rows][4]
+  int2 *splits;             // per CTA: the lane group whose first of several
+                            // parts it has and their number, or -1 (p.finish)
+  int *counters;            // [kCounters], zero at start and end: parts done
+  float2 *lse;              // [B * Hkv][R] (scored): m and 1 / l of every row
+  float *scores;            // [B * Hkv][R][Cp] (scored, few rows), else NULL
   float *weights;           // [B,Hkv,C] (scored), else NULL
   int B, Hq, Hkv, C, d, t, r, R, window, tree;
   int Cp;                   // row pitch of scores: C rounded up to whole tiles
   int group_rows;           // rows one CTA works on (a slot's rows)
   int MG;                   // groups of group_rows rows per lane
-  int ctas, min_tiles;      // tensor-core split (ctas CTAs share all tiles)
+  int ctas, min_tiles, pad; // tensor-core split (ctas CTAs share all tiles)
   int ns;                   // CUDA-core split (ns parts per lane), else 0
+  int finish;               // rows_finish_kernel merges
   float scale_log2;
 };
 
@@ -95,18 +104,31 @@ __device__ __forceinline__ Line line_of(const int32_t *par, int i, int window) {
 
 // ------------------------------------------------- the tensor-core split
 // The tiles of all lanes laid end to end, batch row by batch row, a row's
-// lanes (b, g, group) one after the other; CTA c takes tiles [c per, (c+1)
-// per).  Every CTA computes the same split from the lengths.
+// lane groups (b, g, group) one after the other, each preceded by `pad`
+// virtual tiles that carry no work (what a lane group costs a CTA besides
+// its tiles: queries, mask, O's way out); CTA c takes [c per, (c+1) per).
+// Every CTA computes the same split from the lengths.
+__device__ __forceinline__ int extent_of(const Params &p, int n) {
+  const int nt = tiles_of(p, n);
+  return nt > 0 ? nt + p.pad : 0;
+}
+
 struct Split {
   long long total, per;
 };
 
-// Warp-wide.  `cum` of batch row b: tiles of the rows before it.
-__device__ __forceinline__ Split split_of(const Params &p, int lane) {
+// Warp-wide; the first kLenCache lengths are left in `cache` on the way.
+constexpr int kLenCache = 128;
+__device__ __forceinline__ Split split_of(const Params &p, int lane, int32_t *cache) {
   long long tot = 0;
-  for (int b = lane; b < p.B; b += 32) tot += tiles_of(p, p.seq_lens[b]);
+  for (int b = lane; b < p.B; b += 32) {
+    const int n = p.seq_lens[b];
+    if (b < kLenCache) cache[b] = n;
+    tot += extent_of(p, n);
+  }
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, off);
+  __syncwarp();
   Split s;
   s.total = tot * p.Hkv * p.MG;
   s.per = (s.total + p.ctas - 1) / p.ctas;
@@ -114,137 +136,180 @@ __device__ __forceinline__ Split split_of(const Params &p, int lane) {
   return s;
 }
 
-__device__ __forceinline__ long long tiles_before(const Params &p, int b_end, int lane) {
-  long long tot = 0;
-  for (int b = lane; b < b_end; b += 32) tot += tiles_of(p, p.seq_lens[b]);
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, off);
-  return tot * p.Hkv * p.MG;
+// ----------------------------------------------------------------- counting
+// One counter per lane group in several parts: indexed by the CTA of its
+// first part (tensor cores: a CTA starts at most one such group) or by the
+// group itself (CUDA cores: cut only while there are at most kCounters / 2).
+constexpr int kCounters = 1024;
+
+__device__ __forceinline__ void fence_acq_rel_gpu() {
+  asm volatile("fence.acq_rel.gpu;" ::: "memory");
 }
 
-// The parts of one (b, vl) lane group: np parts in slots s0, s0 + 1, ...
-struct Parts {
-  long long s0;
-  int np;
-};
-
-// vl = g * MG + group.
-__device__ __forceinline__ Parts parts_of(const Params &p, const Split &s, long long cum, int b,
-                                          int vl) {
-  Parts r;
-  const long long L = (long long)b * p.Hkv * p.MG + vl;
-  if (p.ns > 0) {
-    r.s0 = L * p.ns;
-    r.np = p.ns;
-    return r;
+// By one thread, after a barrier behind the stores of the part: true if this
+// was the last of np, whose loads then see every part (after a barrier).
+__device__ __forceinline__ bool count_part(int *counter, int np) {
+  fence_acq_rel_gpu();
+  const bool last = atomicAdd(counter, 1) == np - 1;
+  if (last) {
+    *counter = 0;
+    fence_acq_rel_gpu();
   }
-  const int nt = tiles_of(p, p.seq_lens[b]);
-  const long long first = cum + (long long)vl * nt;
-  const long long c0 = first / s.per;
-  r.s0 = L + c0;
-  r.np = nt == 0 ? 0 : (int)((first + nt - 1) / s.per - c0) + 1;
-  return r;
+  return last;
 }
 
-// ------------------------------------------------------- merge and weights
-constexpr int kFinishThreads = 256;
-constexpr int kFinishCells = 4 * kFinishThreads;  // cells per CTA (weights)
+// A part's weight 2^(m_i - m).  One without keys has l = 0; one whose scores
+// are all NaN has no maximum either, and keeps its sum.
+__device__ __forceinline__ float part_weight(float2 ml, float m) {
+  return ml.x == -INFINITY ? (ml.y != 0.f ? 1.f : 0.f) : exp2f(ml.x - m);
+}
 
-// Blocks [0, merge_blocks): 8 rows each of a lane group; the rest: cells of a
-// lane's weights.
+// Columns [4 c0, ...) of a row over np parts: U groups of 4 columns, wpc
+// apart, J parts in flight.
+template <int U, int J>
+__device__ __forceinline__ void merge_columns(const Params &p, const float2 *ml, const float4 *acc,
+                                              int np, int d4, int wpc, int c0, float m, float *row,
+                                              float *l_out) {
+  float a[U][4], l = 0.f;
+#pragma unroll
+  for (int u = 0; u < U; ++u) a[u][0] = a[u][1] = a[u][2] = a[u][3] = 0.f;
+  for (int j0 = 0; j0 < np; j0 += J) {
+    float2 y[J];
+    float4 v[J][U];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      y[j] = make_float2(-INFINITY, 0.f);
+      if (j0 + j < np) y[j] = __ldcg(&ml[(long long)(j0 + j) * p.group_rows]);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (j0 + j < np && c0 + u * wpc < d4)
+          v[j][u] = __ldcg(&acc[((long long)(j0 + j) * d4 + c0 + u * wpc) * p.group_rows]);
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      if (j0 + j >= np) break;
+      const float e = part_weight(y[j], m);
+      l = fmaf(e, y[j].y, l);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (c0 + u * wpc < d4) {
+          a[u][0] = fmaf(e, v[j][u].x, a[u][0]);
+          a[u][1] = fmaf(e, v[j][u].y, a[u][1]);
+          a[u][2] = fmaf(e, v[j][u].z, a[u][2]);
+          a[u][3] = fmaf(e, v[j][u].w, a[u][3]);
+        }
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;  // 0: no key at all
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (c0 + u * wpc < d4)
+      *reinterpret_cast<float4 *>(row + (c0 + u * wpc) * 4) =
+          make_float4(a[u][0] * inv, a[u][1] * inv, a[u][2] * inv, a[u][3] * inv);
+  *l_out = l;
+}
+
+// Merges np parts (slots s0 ..) of a lane group's nrows (<= 32 NW) rows: into
+// tile[row * pitch + column] in shared memory, and lse.  NW warps; each takes
+// 32 rows and every wpc-th group of 4 columns, a lane per row, so loads are
+// 512 consecutive bytes.  What it takes is round trips to L2 (the parts are
+// other SMs' last stores), so 16 loads are in flight at a time, over columns
+// or over parts.
+template <int NW>
+__device__ __forceinline__ void merge_parts(const Params &p, long long s0, int np, int nrows,
+                                            int warp, float *tile, int pitch, float2 *lse) {
+  const int lane = threadIdx.x & 31;
+  const int chunks = (nrows + 31) / 32, wpc = NW / chunks;  // warps per 32 rows
+  const int chunk = warp / wpc, sub = warp - chunk * wpc;
+  const int row = chunk * 32 + lane, d4 = (p.d + 3) / 4;
+  if (chunk >= chunks || row >= nrows) return;
+  const float2 *ml = p.ml + s0 * p.group_rows + row;
+  float m = -INFINITY, l = 0.f;
+#pragma unroll 8
+  for (int j = 0; j < np; ++j) m = fmaxf(m, __ldcg(&ml[(long long)j * p.group_rows].x));
+  const float4 *acc = reinterpret_cast<const float4 *>(p.acc) + s0 * d4 * p.group_rows + row;
+  if (np <= 4) {
+    for (int c0 = sub; c0 < d4; c0 += 4 * wpc)
+      merge_columns<4, 4>(p, ml, acc, np, d4, wpc, c0, m, tile + row * pitch, &l);
+  } else {
+    for (int c0 = sub; c0 < d4; c0 += 2 * wpc)
+      merge_columns<2, 8>(p, ml, acc, np, d4, wpc, c0, m, tile + row * pitch, &l);
+  }
+  if (lse && sub == 0) lse[row] = make_float2(m == -INFINITY ? 0.f : m, l == 0.f ? 0.f : 1.f / l);
+}
+
+// ------------------------------------------------------------------- finish
+// Block (CTA of the split, 32 rows, 8 groups of 4 columns): a warp has one
+// group of columns, a lane per row, 8 parts in flight.
+constexpr int kFinishThreads = 256;
+constexpr int kFinishRows = 32, kFinishCols = 32;
+
 template <typename T>
 __global__ void __launch_bounds__(kFinishThreads)
-    rows_finish_kernel(const Params p, int merge_blocks, int row_blocks, int cell_blocks) {
-  __shared__ Split s_split;
-  __shared__ long long s_cum;
-  __shared__ float s_m[kFinishThreads], s_inv[kFinishThreads];
+    rows_finish_kernel(const Params p, int row_blocks, int col_blocks) {
+  __shared__ __align__(16) float tile[kFinishRows][kFinishCols + 4];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int LPB = p.Hkv * p.MG;
-  const bool merging = (int)blockIdx.x < merge_blocks;
-  const long long i = merging ? blockIdx.x : blockIdx.x - merge_blocks;
-  const long long lg = merging ? i / row_blocks : i / cell_blocks;  // lane group, or lane
-  const int part = (int)(i - lg * (merging ? row_blocks : cell_blocks));
-  const int b = (int)(lg / (merging ? LPB : p.Hkv));
-  const int x = (int)(lg - (long long)b * (merging ? LPB : p.Hkv));  // vl, or g
-  const int n = p.seq_lens[b];
-  if (!length_ok(p, n)) return;  // its output is zeroed by the split kernel
-  if (!merging && part * kFinishCells >= n) return;
-  if (p.ns == 0 && warp == 0) {
-    const Split s = split_of(p, lane);
-    const long long cum = tiles_before(p, b, lane);
-    if (lane == 0) {
-      s_split = s;
-      s_cum = cum;
-    }
+  int i = blockIdx.x;
+  const int cb = i % col_blocks;
+  i /= col_blocks;
+  const int rb = i % row_blocks, c = i / row_blocks;
+  const int2 x = p.splits[c];
+  if (x.x < 0) return;
+  const int ln = x.x / p.MG, grp = x.x - ln * p.MG, np = x.y;
+  const int rho0 = grp * p.group_rows + rb * kFinishRows;  // first row of the lane
+  const int nrows = min(min(kFinishRows, p.group_rows - rb * kFinishRows), p.R - rho0);
+  if (nrows <= 0) return;
+  const int d4 = p.d / 4, c4 = cb * (kFinishCols / 4) + warp;  // d is 64 or 128
+  if (lane < nrows) {
+    const long long s0 = (long long)x.x + c;  // the first part's slot
+    const int row = rb * kFinishRows + lane;
+    const float2 *ml = p.ml + s0 * p.group_rows + row;
+    const float4 *acc = reinterpret_cast<const float4 *>(p.acc) + s0 * d4 * p.group_rows + row;
+    float m = -INFINITY, l;
+#pragma unroll 8
+    for (int j = 0; j < np; ++j) m = fmaxf(m, ml[(long long)j * p.group_rows].x);
+    merge_columns<1, 8>(p, ml, acc, np, d4, 1, c4, m, &tile[lane][0] - cb * kFinishCols, &l);
+    if (p.lse && c4 == 0)
+      p.lse[(long long)ln * p.R + rho0 + lane] =
+          make_float2(m == -INFINITY ? 0.f : m, l == 0.f ? 0.f : 1.f / l);
   }
   __syncthreads();
-
-  if (merging) {
-    const Parts pt = parts_of(p, s_split, s_cum, b, x);
-    const int g = x / p.MG, grp = x - g * p.MG;
-    const int row = part * (kFinishThreads / 32) + warp;  // in the group
-    const int rho = grp * p.group_rows + row;
-    if (pt.np <= 1 || row >= p.group_rows || rho >= p.R) return;
-    float m = -INFINITY;
-    for (int j = lane; j < pt.np; j += 32) m = fmaxf(m, p.ml[(pt.s0 + j) * p.group_rows + row].x);
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    float l = 0.f, a[GQA_MAX_HEAD_DIM / 32];
-#pragma unroll
-    for (int c = 0; c < GQA_MAX_HEAD_DIM / 32; ++c) a[c] = 0.f;
-    const float *acc = p.acc + (pt.s0 * p.group_rows + row) * p.d;
-    const long long step = (long long)p.group_rows * p.d;
-    for (int j0 = 0; j0 < pt.np; j0 += 32) {
-      const int nj = min(32, pt.np - j0);
-      float e = 0.f, lw = 0.f;
-      if (lane < nj) {
-        const float2 y = p.ml[(pt.s0 + j0 + lane) * p.group_rows + row];
-        // a part without keys has l = 0; one whose scores are all NaN keeps it
-        e = y.x == -INFINITY ? (y.y != 0.f ? 1.f : 0.f) : exp2f(y.x - m);
-        lw = y.y;
-      }
-#pragma unroll 4
-      for (int j = 0; j < nj; ++j) {
-        const float ej = __shfl_sync(0xffffffffu, e, j), lj = __shfl_sync(0xffffffffu, lw, j);
-        if (ej == 0.f) continue;  // an empty part: its acc is not written
-        l = fmaf(ej, lj, l);
-#pragma unroll
-        for (int c = 0; c < GQA_MAX_HEAD_DIM / 32; ++c)
-          if (c * 32 + lane < p.d) a[c] = fmaf(ej, acc[(j0 + j) * step + c * 32 + lane], a[c]);
-      }
-    }
-    T *o = (T *)p.o + (((long long)b * p.Hq + (long long)g * p.r) * p.t + rho) * p.d;
-    const float inv = 1.f / l;
-    const bool dead = l == 0.f;  // no key at all: zero
-#pragma unroll
-    for (int c = 0; c < GQA_MAX_HEAD_DIM / 32; ++c)
-      if (c * 32 + lane < p.d) o[c * 32 + lane] = from_f32<T>(dead ? 0.f : a[c] * inv);
-    return;
+  T *o = (T *)p.o + ((long long)ln * p.R + rho0) * p.d + cb * kFinishCols;
+  for (int e = threadIdx.x; e < nrows * (kFinishCols / 2); e += kFinishThreads) {
+    const int k = e / (kFinishCols / 2), col = 2 * (e % (kFinishCols / 2));
+    *reinterpret_cast<uint32_t *>(o + (long long)k * p.d + col) =
+        pack_bf16(tile[k][col], tile[k][col + 1]);
   }
+}
 
+// ------------------------------------------------------------------ weights
+constexpr int kWeighThreads = 256;
+constexpr int kWeighCells = 4 * kWeighThreads;  // cells per CTA
+
+__global__ void __launch_bounds__(kWeighThreads) rows_weigh_kernel(const Params p, int cell_blocks) {
+  __shared__ float s_m[kWeighThreads], s_inv[kWeighThreads];
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const int ln = blockIdx.x / cell_blocks, part = blockIdx.x - ln * cell_blocks;  // lane (b, g)
+  const int b = ln / p.Hkv, g = ln - b * p.Hkv;
+  const int n = p.seq_lens[b];
+  if (!length_ok(p, n) || part * kWeighCells >= n) return;
   // weights of cells [j, j + 4) of lane (b, g)
-  const int g = x, j = part * kFinishCells + threadIdx.x * 4;
+  const int j = part * kWeighCells + threadIdx.x * 4;
   float w[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int r0 = 0; r0 < p.R; r0 += kFinishThreads) {
+  for (int r0 = 0; r0 < p.R; r0 += kWeighThreads) {
     const int rho = r0 + threadIdx.x;
     __syncthreads();
     if (rho < p.R) {
-      const int grp = rho / p.group_rows, row = rho - grp * p.group_rows;
-      const Parts pt = parts_of(p, s_split, s_cum, b, g * p.MG + grp);
-      float m = -INFINITY, l = 0.f;
-      for (int k = 0; k < pt.np; ++k) m = fmaxf(m, p.ml[(pt.s0 + k) * p.group_rows + row].x);
-      for (int k = 0; k < pt.np; ++k) {
-        const float2 y = p.ml[(pt.s0 + k) * p.group_rows + row];
-        l = fmaf(y.x == -INFINITY ? (y.y != 0.f ? 1.f : 0.f) : exp2f(y.x - m), y.y, l);
-      }
-      s_m[threadIdx.x] = m == -INFINITY ? 0.f : m;
-      s_inv[threadIdx.x] = l == 0.f ? 0.f : 1.f / l;
+      const float2 y = p.lse[(long long)ln * p.R + rho];
+      s_m[threadIdx.x] = y.x;
+      s_inv[threadIdx.x] = y.y;
     }
     __syncthreads();
     if (j >= n) continue;
-    const int nr = min(kFinishThreads, p.R - r0);
+    const int nr = min(kWeighThreads, p.R - r0);
     const float *s = p.scores + ((long long)(b * p.Hkv + g) * p.R + r0) * p.Cp + j;
 #pragma unroll 4
     for (int k = 0; k < nr; ++k) {

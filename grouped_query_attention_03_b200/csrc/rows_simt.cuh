@@ -28,6 +28,7 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const Params p)
   extern __shared__ __align__(16) float sm[];
   __shared__ int32_t s_par[kMaxNodes];
   __shared__ float s_alpha[kSR], s_ml[kSR][2];
+  __shared__ int s_last;
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int pitch = simt_pitch(p.d), d4 = (p.d + 3) / 4;
@@ -200,23 +201,43 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const Params p)
     }
   }
   __syncthreads();
-  if (tid < nrows && (p.ns > 1 || p.scores))
-    p.ml[slot * kSR + tid] = make_float2(s_ml[tid][0], s_ml[tid][1]);
+  if (p.ns == 1) {
+    if (p.lse && tid < nrows) {
+      const float mk = s_ml[tid][0], lk = s_ml[tid][1];
+      p.lse[ln * p.R + rho0 + tid] =
+          make_float2(mk == -INFINITY ? 0.f : mk, lk == 0.f ? 0.f : 1.f / lk);
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int col = tid + c * kSimtThreads;
+      if (col >= p.d) continue;
+#pragma unroll
+      for (int k = 0; k < kSR; ++k) {
+        if (k >= nrows) continue;
+        const float lk = s_ml[k][1];
+        o[(long long)k * p.d + col] = from_f32<T>(lk == 0.f ? 0.f : acc[c][k] / lk);  // 0: no keys
+      }
+    }
+    return;
+  }
+  if (tid < nrows) p.ml[slot * kSR + tid] = make_float2(s_ml[tid][0], s_ml[tid][1]);
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const int col = tid + c * kSimtThreads;
     if (col >= p.d) continue;
 #pragma unroll
-    for (int k = 0; k < kSR; ++k) {
-      if (k >= nrows) continue;
-      if (p.ns > 1) {
-        p.acc[(slot * kSR + k) * p.d + col] = acc[c][k];
-      } else {
-        const float lk = s_ml[k][1];
-        o[(long long)k * p.d + col] = from_f32<T>(lk == 0.f ? 0.f : acc[c][k] / lk);  // 0: no keys
-      }
-    }
+    for (int k = 0; k < kSR; ++k)
+      if (k < nrows) p.acc[((slot * d4 + col / 4) * kSR + k) * 4 + (col & 3)] = acc[c][k];
   }
+  __syncthreads();
+  if (tid == 0) s_last = count_part(&p.counters[L], p.ns);
+  __syncthreads();
+  if (!s_last) return;
+  merge_parts<kSimtThreads / 32>(p, L * p.ns, p.ns, nrows, warp, sm, pitch,
+                                 p.lse ? p.lse + ln * p.R + rho0 : nullptr);
+  __syncthreads();
+  for (int k = warp; k < nrows; k += kSimtThreads / 32)
+    for (int c = lane; c < p.d; c += 32) o[(long long)k * p.d + c] = from_f32<T>(sm[k * pitch + c]);
 }
 
 }  // namespace rows

@@ -12,12 +12,17 @@
 //   warp 1      one lane issues tcgen05.mma: S = Q K^T (M = N = 128, K = d)
 //               into TMEM, and O += P V with P read from TMEM
 //   warp 2      zeroes the outputs of refused sequences, reports them
-//   4 NT warps  softmax, one thread per row: loads its S row, masks edge
-//               tiles, rescales O when its maximum grew by more than 2^8,
-//               writes bf16 P over S; at the end of a segment the O row goes
-//               out (a lane group in one part) or to the workspace
+//   warps 4-11  softmax.  NT = 1: two warpgroups, each with 64 of a tile's
+//               128 keys, a thread per row, with its own running maximum, sum
+//               and O, combined once at the end of a segment; NT = 2: a
+//               warpgroup per row tile, a thread per row with all 128 keys.
+//               A thread loads its scores, masks edge tiles, rescales O when
+//               its maximum grew by more than 2^8 and writes bf16 P over S;
+//               at the end of a segment the O row goes out (a lane group in
+//               one part) or to the workspace.
 // TMEM: NT = 1 has two S buffers, so S(j+1) is computed under the softmax of
-// tile j; NT = 2 has one per row tile, and the two tiles take turns.
+// tile j, and two O; NT = 2 has one S and one O per row tile, and the two
+// take turns.
 //
 // Bound by HBM while a group has at most about 256 rows: a 128-key tile is
 // 4 d * 128 bytes, 1.5 us of an SM's share of the bandwidth at d = 128,
@@ -42,15 +47,17 @@ namespace rows {
 constexpr int kM = 128;                    // rows per row tile
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLazyRescale = 8.0f;       // log2 units
-// Registers per thread of the NT = 2 kernel after the split: 128 * low + 256 *
-// high must not exceed its 384 threads times the 168 they are launched with.
+constexpr int kTcThreads = 384;
+// Registers per thread after the split: 128 * low + 256 * high must not exceed
+// the 384 threads times the 168 they are launched with.
 constexpr int kRegsLow = 72, kRegsHigh = 216;
 static_assert(128 * kRegsLow + 256 * kRegsHigh <= 384 * 168, "register split");
+constexpr int kAddParts = 4;               // parts a CTA adds to its own O at most
 constexpr int kUnfinite = 4;               // edge tiles of a segment at most
 
 template <int D, int NT>
 struct TcCfg {
-  static constexpr int THREADS = 128 + 128 * NT;
+  static constexpr int NC = NT == 1 ? 64 : 128;  // keys of a tile per softmax thread
   static constexpr int KB = D / 64;            // 64-column blocks
   static constexpr int BLK = 128 * 128;        // 128 rows x 128 B
   static constexpr int TILE = KB * BLK;        // a Q, K or V tile
@@ -61,7 +68,7 @@ struct TcCfg {
   static constexpr int OFF_V = OFF_K + STAGES * TILE;
   static constexpr int SMEM = OFF_V + STAGES * TILE + 1024;  // + alignment
   static constexpr uint32_t TM_O = 256;
-  static_assert(TM_O + NT * D <= kTmemCols, "S and O must fit in TMEM");
+  static_assert(TM_O + 2 * D <= kTmemCols, "S and O must fit in TMEM");
 };
 
 struct Unfinite {  // value rows of one edge tile cleared for the MMA
@@ -69,44 +76,76 @@ struct Unfinite {  // value rows of one edge tile cleared for the MMA
   uint32_t bits[4];
 };
 
+// A lane group in several parts: its first part's CTA and their number.
+struct Group {
+  long long L;
+  int c0, np;
+};
 struct TcShared {
   uint64_t q_full, q_empty;
   uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
-  uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+  uint64_t s_full[2], o_done[2], o_free[2];
+  uint64_t p_full[2][2];   // [S buffer][key half]: P of these 64 keys written
   uint64_t mma_fin;
+  uint64_t early_full, early_done;  // the first segment's part: written, counted
   uint32_t tmem;
-  int b, vl, tile;         // where this CTA's range starts
+  int b, vl, off;          // where this CTA's range starts
   long long start, end;    // its tiles
-  Split split;
+  long long per;           // tiles of every CTA
+  int early_last;             // that part was its group's last
+  Group late;                 // the last segment's group, to be merged
+  int32_t len[kLenCache];
   Unfinite unfinite[kUnfinite];
   int32_t par[2][kMaxNodes];
 };
 
 // A run of one lane group's tiles in this CTA's range.
 struct Seg {
+  long long first;       // where the lane group's first tile is, over all CTAs
   int b, vl, n, ntiles;  // ntiles: of the whole lane group
   int j0, j1;            // this segment's tiles
 };
 
+__device__ __forceinline__ Group group_of(const Params &p, const Seg &sg, long long per) {
+  Group r;
+  r.L = (long long)sg.b * p.Hkv * p.MG + sg.vl;
+  r.c0 = (int)(sg.first / per);
+  r.np = (int)((sg.first + sg.ntiles - 1) / per) - r.c0 + 1;
+  return r;
+}
+// The first segment, when it ends a lane group that began in an earlier CTA
+// and others follow: its part is counted as soon as it is written.
+__device__ __forceinline__ bool is_early(const Params &p, const Seg &sg, bool first, bool more) {
+  return !p.finish && first && more && sg.j0 > 0;
+}
+
 // Walks the CTA's range segment by segment; every role has its own.
 struct Walk {
-  int b, vl, tile;
+  int b, vl, off;          // off: into the lane group's extent, pad first
   long long pos, end;
+  const int32_t *cached;   // the lengths in shared memory
   __device__ __forceinline__ bool next(const Params &p, Seg *s) {
-    if (pos >= end) return false;
     while (true) {
-      if (b >= p.B) return false;
-      s->n = p.seq_lens[b];
+      if (pos >= end || b >= p.B) return false;
+      s->n = b < kLenCache ? cached[b] : p.seq_lens[b];
       s->ntiles = tiles_of(p, s->n);
-      if (s->ntiles > 0) break;
-      ++b;  // a refused sequence has no tiles (pos < end: a later one has)
+      if (s->ntiles > 0) {
+        const int skip = max(0, p.pad - off);
+        pos += skip;
+        off += skip;
+        break;
+      }
+      ++b;  // a refused sequence has no tiles
+      vl = 0;
     }
+    if (pos >= end) return false;
     s->b = b;
     s->vl = vl;
-    s->j0 = tile;
-    s->j1 = (int)min((long long)s->ntiles, tile + (end - pos));
+    s->j0 = off - p.pad;
+    s->first = pos - s->j0;
+    s->j1 = (int)min((long long)s->ntiles, s->j0 + (end - pos));
     pos += s->j1 - s->j0;
-    tile = 0;
+    off = 0;
     if (++vl == p.Hkv * p.MG) {
       vl = 0;
       ++b;
@@ -157,33 +196,69 @@ __device__ __forceinline__ uint32_t s_phase(int kx) {
   return (uint32_t)(NT == 1 ? (kx >> 1) & 1 : kx & 1);
 }
 
-// Whether any of the `threads` softmax threads says so (and a barrier).
-__device__ __forceinline__ bool any_of_softmax(bool mine, int threads) {
+__device__ __forceinline__ uint64_t l2_policy_normal() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+
+// tma_load_3d with an L2 cache policy.
+__device__ __forceinline__ void tma_load_3d_hint(void *smem_dst, const CUtensorMap *map, int c0,
+                                                 int c1, int c2, uint64_t *bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_"
+      "tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)),
+      "l"(policy)
+      : "memory");
+}
+
+// Two 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st2(uint32_t taddr, float a, float b) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr),
+               "r"(__float_as_uint(a)), "r"(__float_as_uint(b))
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld2(uint32_t taddr, float &a, float &b) {
+  uint32_t x, y;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];"
+               : "=r"(x), "=r"(y)
+               : "r"(taddr));
+  a = __uint_as_float(x);
+  b = __uint_as_float(y);
+}
+
+// Whether any of the `threads` softmax threads says so (and a barrier).  The
+// end of the kernel has a barrier of its own: the second warpgroup may be
+// there while the first is still in a segment that is its alone.
+constexpr int kBarSegment = 3, kBarEnd = 4;
+__device__ __forceinline__ bool any_of_softmax(bool mine, int threads, int bar = kBarSegment) {
   uint32_t r;
   asm volatile(
       "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
-      " barrier.cta.red.or.pred q, 3, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+      " barrier.cta.red.or.pred q, %3, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
       : "=r"(r)
-      : "r"((uint32_t)mine), "r"(threads)
+      : "r"((uint32_t)mine), "r"(threads), "r"(bar)
       : "memory");
   return r != 0;
 }
 
 // The value rows that were cleared for the MMA although they are somebody's:
-// adds 2^(s - m) v to this thread's O row (TMEM) where it may read them.
+// adds 2^(s - m) v to this thread's O row (TMEM) where it may read them, for
+// keys [e_first, e_last) of the tiles.
 // Warp-wide; rare, so keys and values come from global memory one by one.
 template <int D>
 __device__ __forceinline__ void add_unfinite(const Params &p, const TcShared &sh, const Seg &sg,
                                              bool mine, int lo, int hi, int lo0, int ncell_tiles,
                                              const Line &line, long long orow, float m_run,
-                                             uint32_t tO) {
+                                             uint32_t tO, int e_first, int e_last) {
   const __nv_bfloat16 *q = (const __nv_bfloat16 *)p.q + (mine ? orow : 0) * D;
   const long long ln = (long long)sg.b * p.Hkv + sg.vl / p.MG;
   for (int k = 0; k < kUnfinite; ++k) {
     const int j = sh.unfinite[k].tile;
     if (j < 0) continue;
     const bool draft = j >= ncell_tiles;
-    for (int e = 0; e < kTile; ++e) {
+    for (int e = e_first; e < e_last; ++e) {
       if (!((sh.unfinite[k].bits[e >> 5] >> (e & 31)) & 1u)) continue;
       const int cell = lo0 + j * kTile + e;
       uint32_t word = 0u;
@@ -218,8 +293,55 @@ __device__ __forceinline__ void add_unfinite(const Params &p, const TcShared &sh
   }
 }
 
+// 32 columns of this thread's O: NT = 1 combines the two halves' (a0, a1).
+// Zero without keys, whatever the MMA made of it.
 template <int D, int NT>
-__global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
+__device__ __forceinline__ void load_o(uint32_t taddr, float a0, float a1, bool none, float *ov) {
+  tc::tmem_ld32(taddr, ov);
+  if constexpr (NT == 1) {
+    float ow[32];
+    tc::tmem_ld32(taddr + D, ow);
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) ov[e] = none ? 0.f : ov[e] * a0 + ow[e] * a1;
+  } else {
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) ov[e] = none ? 0.f : ov[e];
+  }
+}
+
+__device__ __forceinline__ int ld_acquire_gpu(const int *p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// Merges a lane group's parts and writes its rows: the 256 softmax threads,
+// through the K and V rings.
+template <int D>
+__device__ __forceinline__ void merge_group(const Params &p, const Group &gr, unsigned char *smem,
+                                         int warp) {
+  const long long ln = gr.L / p.MG;
+  const int grp = (int)(gr.L - ln * p.MG);
+  const int rows = min(p.group_rows, p.R - grp * p.group_rows);
+  const long long row0 = ln * p.R + (long long)grp * p.group_rows;
+  float *tile = reinterpret_cast<float *>(smem);
+  constexpr int pitch = D + 4;
+  merge_parts<8>(p, gr.L + gr.c0, gr.np, rows, warp, tile, pitch, p.lse ? p.lse + row0 : nullptr);
+  any_of_softmax(false, 256, kBarEnd);
+  __nv_bfloat16 *o = (__nv_bfloat16 *)p.o + row0 * D;
+  for (int e = (threadIdx.x - 128) * 8; e < rows * D; e += 256 * 8) {
+    const float *src = tile + (e / D) * pitch + e % D;
+    *reinterpret_cast<uint4 *>(o + e) =
+        make_uint4(pack_bf16(src[0], src[1]), pack_bf16(src[2], src[3]), pack_bf16(src[4], src[5]),
+                   pack_bf16(src[6], src[7]));
+  }
+  any_of_softmax(false, 256, kBarEnd);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kTcThreads, 1)
     rows_splitk_kernel(const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV,
@@ -243,11 +365,14 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sh.s_full[s], 1);
-      mbar_init(&sh.p_full[s], 4);  // a row tile's four warps
+      mbar_init(&sh.p_full[s][0], 4);  // a warpgroup's four warps
+      mbar_init(&sh.p_full[s][1], 4);
       mbar_init(&sh.o_done[s], 1);
-      mbar_init(&sh.o_free[s], 4);
+      mbar_init(&sh.o_free[s], NT == 1 ? 8 : 4);  // the warps that read O_x
     }
     mbar_init(&sh.mma_fin, 1);
+    mbar_init(&sh.early_full, 8);
+    mbar_init(&sh.early_done, 1);
     for (int k = 0; k < kUnfinite; ++k) sh.unfinite[k] = Unfinite{-1, {0u, 0u, 0u, 0u}};
     fence_mbar_init();
   }
@@ -268,15 +393,16 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
   if (threadIdx.x == 0) griddep_launch_dependents();
   if (warp == 0) {
     // this CTA's range, and the lane group and tile it starts in
-    const Split s = split_of(p, lane);
+    const Split s = split_of(p, lane, sh.len);
     const long long start = (long long)blockIdx.x * s.per, end = min(s.total, start + s.per);
     const long long LPB = (long long)p.Hkv * p.MG;
     long long cum = 0;
-    int b = 0, vl = 0, tile = 0;
+    int b = 0, vl = 0, off0 = 0;
     if (start < end) {
       for (int b0 = 0; b0 < p.B; b0 += 32) {
         const int bb = b0 + lane;
-        const long long x = bb < p.B ? tiles_of(p, p.seq_lens[bb]) * LPB : 0;
+        const long long x =
+            bb < p.B ? extent_of(p, bb < kLenCache ? sh.len[bb] : p.seq_lens[bb]) * LPB : 0;
         long long incl = x;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -288,21 +414,22 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
           const int src = __ffs(hit) - 1;
           b = b0 + src;
           cum += __shfl_sync(0xffffffffu, incl - x, src);
-          const long long nt = __shfl_sync(0xffffffffu, x, src) / LPB;
-          vl = (int)((start - cum) / nt);
-          tile = (int)((start - cum) - vl * nt);
+          const int ext = (int)(__shfl_sync(0xffffffffu, x, src) / LPB);
+          vl = (int)((start - cum) / ext);
+          off0 = (int)((start - cum) - (long long)vl * ext);
           break;
         }
         cum += __shfl_sync(0xffffffffu, incl, 31);
       }
     }
+    if (lane == 1 && p.finish) p.splits[blockIdx.x] = make_int2(-1, 0);
     if (lane == 0) {
       sh.b = b;
       sh.vl = vl;
-      sh.tile = tile;
+      sh.off = off0;
       sh.start = start;
       sh.end = end;
-      sh.split = s;
+      sh.per = s.per;
     }
   }
   tc::fence_before_sync();
@@ -310,18 +437,34 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
   tc::fence_after_sync();
   const uint32_t tmem = sh.tmem;
   bool failed = false;
-  Walk walk{sh.b, sh.vl, sh.tile, sh.start, sh.end};
+  Walk walk{sh.b, sh.vl, sh.off, sh.start, sh.end, sh.len};
   Seg sg;
 
   if (warp >= 4) {
     // ================================================= softmax: one row each
-    if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
-    const int x = (warp - 4) >> 2;           // row tile
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
+    constexpr int NC = K::NC;
+    const int wg = (warp - 4) >> 2;          // warpgroup
+    const int x = NT == 1 ? 0 : wg;          // row tile
+    const int e0 = NT == 1 ? wg * NC : 0;    // first key of a tile
     const int q4 = warp & 3;                 // TMEM lane quarter
-    const int row = q4 * 32 + lane;          // row within the tile
+    const int row = q4 * 32 + lane;          // row within the row tile
     const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
-    const uint32_t tO = tmem + lane_base + K::TM_O + x * D;
-    const float sc = p.scale_log2;
+    const uint32_t tO = tmem + lane_base + K::TM_O + wg * D;
+    // Scores are compared as they come and scaled in the exponent's FMA; a
+    // negative scale turns the order around, and 0 is a scale too small to
+    // show.  A masked score is the infinity that the scale makes negative.
+    const float sc = p.scale_log2 == 0.f ? 1e-30f : p.scale_log2;
+    const bool neg = sc < 0.f;
+    const float masked = neg ? INFINITY : -INFINITY;
+    bool first_seg = true;
+    int left = 0;                            // the last segment's part was left behind
+    int was_b = -1, was_grp = -1;            // whose masks `line`, lo, hi are
+    int lo = 0, hi = 0;                      // cells [lo, hi) this row may read
+    Line line;
+    line.depth = -1;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) line.bits[w] = 0u;
     int jj = 0;                              // tiles of the range so far
     int jx = 0;                              // of these, with rows in this row tile
     bool ok = true;
@@ -329,43 +472,47 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
       const int g = sg.vl / p.MG, grp = sg.vl - g * p.MG;
       const int rho_x = grp * p.group_rows + x * kM;   // the row tile's first row
       const int nx = min(NT, (p.R - grp * p.group_rows + kM - 1) / kM);  // row tiles here
+      const bool more = walk.pos < walk.end;           // segments may follow
+      const bool is_e = is_early(p, sg, first_seg, more);
+      first_seg = false;
       if (x >= nx) {  // no rows in this tile: it takes no part in the segment
         jj += sg.j1 - sg.j0;
+        if (is_e && lane == 0) mbar_arrive(&sh.early_full);
         continue;
       }
       const int rho = rho_x + row;
       const bool mine = rho < p.R;
       const bool warp_on = rho_x + q4 * 32 < p.R;      // any row of this warp
-      const int i = mine ? rho % p.t : 0;
       const int lo0 = first_cell(p, sg.n);
-      // what this row may read
-      int lo = 0, hi = 0;  // cells [lo, hi)
-      Line line;
-      line.depth = -1;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) line.bits[w] = 0u;
-      if (p.tree) {
-        if (p.parents) {
-          // the previous segment's readers are past their masks here
-          asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
-          if (row < p.t) sh.par[x][row] = p.parents[(long long)sg.b * p.t + row];
-          asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
-        }
-        if (mine) {
-          line = line_of(p.parents ? sh.par[x] : nullptr, i, p.window);
-          if (line.refused) record_status(p.status, GQA_ERR_TREE);
-          if (line.depth >= 0) {
-            lo = p.window > 0 ? max(0, sg.n + line.depth - (p.window - 1)) : 0;
-            hi = sg.n;
+      // what this row may read: the same for all lanes of a sequence
+      if (sg.b != was_b || grp != was_grp) {
+        const int i = mine ? rho % p.t : 0;
+        lo = hi = 0;
+        if (p.tree) {
+          if (p.parents && sg.b != was_b) {
+            // the previous segment's readers are past their masks here
+            asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
+            if (row < p.t) sh.par[wg][row] = p.parents[(long long)sg.b * p.t + row];
+            asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
           }
+          if (mine) {
+            line = line_of(p.parents ? sh.par[wg] : nullptr, i, p.window);
+            if (line.refused) record_status(p.status, GQA_ERR_TREE);
+            if (line.depth >= 0) {
+              lo = p.window > 0 ? max(0, sg.n + line.depth - (p.window - 1)) : 0;
+              hi = sg.n;
+            }
+          }
+        } else if (mine) {
+          hi = sg.n - p.t + i + 1;
         }
-      } else if (mine) {
-        hi = sg.n - p.t + i + 1;
+        was_b = sg.b;
+        was_grp = grp;
       }
       const int ncell_tiles = sg.ntiles - p.tree;
       float m_run = -INFINITY, l_run = 0.f;
       float *srow = p.scores && mine
-                        ? p.scores + (((long long)sg.b * p.Hkv + g) * p.R + rho) * p.Cp
+                        ? p.scores + (((long long)sg.b * p.Hkv + g) * p.R + rho) * p.Cp + e0
                         : nullptr;
       bool found = false;  // value rows cleared that are not finite
       for (int j = sg.j0; j < sg.j1; ++j, ++jj, ++jx) {
@@ -375,93 +522,21 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
         // tiles that some row may not read all of
         const bool edge = draft || c0 + kTile > (p.tree ? sg.n : sg.n - p.t + 1) ||
                           (p.window > 0 && c0 < sg.n + p.t - p.window);
-        if (!__all_sync(0xffffffffu, mbar_wait(&sh.s_full[sb], s_phase<NT>(jx), &failed))) {
+        if (!__all_sync(0xffffffffu, mbar_wait_spin(&sh.s_full[sb], s_phase<NT>(jx), &failed))) {
           ok = false;
           break;
         }
         tc::fence_after_sync();
-        const uint32_t tS = tmem + lane_base + sb * kTile;
-        if (warp_on) {
-          float s[kTile];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tc::tmem_ld32(tS + c * 32, s + c * 32);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < kTile; ++e) s[e] *= sc;
-          if (edge) {
-            if (draft) {
-#pragma unroll
-              for (int e = 0; e < kTile; ++e)
-                if (!((line.bits[e >> 5] >> (e & 31)) & 1u)) s[e] = -INFINITY;
-            } else {
-              const int a = lo - c0, z = hi - c0;
-#pragma unroll
-              for (int e = 0; e < kTile; ++e)
-                if (e < a || e >= z) s[e] = -INFINITY;
-            }
-          }
-          if (srow) {
-#pragma unroll
-            for (int e = 0; e < kTile; e += 4)
-              *reinterpret_cast<float4 *>(srow + c0 + e) = make_float4(s[e], s[e + 1], s[e + 2], s[e + 3]);
-          }
-          float mc[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int e = 0; e < kTile; e += 2) mc[(e >> 1) & 3] = fmax3(mc[(e >> 1) & 3], s[e], s[e + 1]);
-          const float m_tile = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
-          if (j == sg.j0) {
-            m_run = m_tile;
-          } else if (__any_sync(0xffffffffu, m_tile > m_run + kLazyRescale)) {
-            // O must hold P V of the previous tile before it is rescaled
-            if (!__all_sync(0xffffffffu, mbar_wait(&sh.o_done[s_buffer<NT>(jx - 1, x)],
-                                                   s_phase<NT>(jx - 1), &failed))) {
-              ok = false;
-              break;
-            }
-            tc::fence_after_sync();
-            const float m_new = fmaxf(m_run, m_tile);
-            const float alpha = m_new == m_run ? 1.f : exp2f(m_run - m_new);
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              float ov[32];
-              tc::tmem_ld32(tO + c * 32, ov);
-              tc::tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) ov[e] *= alpha;
-              tc::tmem_st32(tO + c * 32, ov);
-            }
-            tc::tmem_wait_st();
-            l_run *= alpha;
-            m_run = m_new;
-          }
-          // bf16 P over the first 64 of S's columns.  The sum takes the fp32
-          // values: their roundings to bf16 are independent and average out.
-          const float msub = m_run == -INFINITY ? 0.f : m_run;
-          float2 lsum = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float w[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float2 pv = make_float2(ex2_approx(s[c * 64 + 2 * e] - msub),
-                                            ex2_approx(s[c * 64 + 2 * e + 1] - msub));
-              lsum = fadd2v(lsum, pv);
-              w[e] = __uint_as_float(pack_bf16(pv.x, pv.y));
-            }
-            tc::tmem_st32(tS + c * 32, w);
-          }
-          tc::tmem_wait_st();
-          l_run += lsum.x + lsum.y;
-        }
-        if (edge && x == 0) {
+        if (edge && (NT == 1 ? (q4 >> 1) == wg : wg == 0)) {
           // value rows that some row may not read: row `row` of the V tile
+          // (NT = 1: by the warps of its own key half)
           const int st = jj % K::STAGES;
           const bool vok = mbar_wait(&sh.v_full[st], (jj / K::STAGES) & 1, &failed);
           bool used;
           if (!draft) {
             used = c0 + row < sg.n;
           } else {
-            used = row < p.t && (!p.parents || sh.par[0][row] != -2);
+            used = row < p.t && (!p.parents || sh.par[wg][row] != -2);
           }
           bool odd = false;
           if (vok) odd = clear_value_row<D>(smem + K::OFF_V + st * K::TILE, row, used);
@@ -483,52 +558,258 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
             break;
           }
         }
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_full[sb]);
+        const uint32_t tS = tmem + lane_base + sb * kTile + e0;
+        if (!warp_on) {  // no rows: nothing to write, but counted
+          if (lane == 0) {
+            mbar_arrive(&sh.p_full[sb][NT == 1 ? wg : 0]);
+            if (NT == 2) mbar_arrive(&sh.p_full[sb][1]);
+          }
+        } else {
+          float s[NC];
+#pragma unroll
+          for (int c = 0; c < NC / 32; ++c) tc::tmem_ld32(tS + c * 32, s + c * 32);
+          tc::tmem_wait_ld();
+          if (edge) {
+            if (draft) {
+#pragma unroll
+              for (int w = 0; w < NC / 32; ++w) {
+                const uint32_t bits = NT == 1 ? (wg ? line.bits[2 + w] : line.bits[w]) : line.bits[w];
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!((bits >> e) & 1u)) s[w * 32 + e] = masked;
+              }
+            } else {
+              const int a = lo - c0 - e0, z = hi - c0 - e0;
+#pragma unroll
+              for (int e = 0; e < NC; ++e)
+                if (e < a || e >= z) s[e] = masked;
+            }
+          }
+          if (srow) {
+#pragma unroll
+            for (int e = 0; e < NC; e += 4)
+              *reinterpret_cast<float4 *>(srow + c0 + e) =
+                  make_float4(s[e] * sc, s[e + 1] * sc, s[e + 2] * sc, s[e + 3] * sc);
+          }
+          float mx;
+          {
+            float mc[4] = {masked, masked, masked, masked};
+            if (!neg) {
+#pragma unroll
+              for (int e = 0; e < NC; e += 2) mc[(e >> 1) & 3] = fmax3(mc[(e >> 1) & 3], s[e], s[e + 1]);
+              mx = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < NC; ++e) mc[e & 3] = fminf(mc[e & 3], s[e]);
+              mx = fminf(fminf(mc[0], mc[1]), fminf(mc[2], mc[3]));
+            }
+          }
+          const float m_tile = mx * sc;  // -inf where every score is masked
+          if (j == sg.j0) {
+            m_run = m_tile;
+          } else if (__any_sync(0xffffffffu, m_tile > m_run + kLazyRescale)) {
+            // O must hold P V of the previous tile before it is rescaled
+            if (!__all_sync(0xffffffffu, mbar_wait_spin(&sh.o_done[s_buffer<NT>(jx - 1, x)],
+                                                   s_phase<NT>(jx - 1), &failed))) {
+              ok = false;
+              break;
+            }
+            tc::fence_after_sync();
+            const float m_new = fmaxf(m_run, m_tile);
+            const float alpha = m_new == m_run ? 1.f : exp2f(m_run - m_new);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              float ov[32];
+              tc::tmem_ld32(tO + c * 32, ov);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ov[e] *= alpha;
+              tc::tmem_st32(tO + c * 32, ov);
+            }
+            tc::tmem_wait_st();
+            l_run *= alpha;
+            m_run = m_new;
+          }
+          // bf16 P over the first half of this thread's S columns.  The sum
+          // takes the fp32 values: their roundings to bf16 are independent
+          // and average out.
+          const float msub = m_run == -INFINITY ? 0.f : m_run;
+          const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-msub, -msub);
+          float2 lsum = make_float2(0.f, 0.f);
+          // published 64 keys at a time: the P V of the first half starts under
+          // the exponentials of the second (NT = 2)
+#pragma unroll
+          for (int c = 0; c < NC / 64; ++c) {
+            float w[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float2 v = ffma2v(make_float2(s[c * 64 + 2 * e], s[c * 64 + 2 * e + 1]), sc2, nm2);
+              const float2 pv = make_float2(ex2_approx(v.x), ex2_approx(v.y));
+              lsum = fadd2v(lsum, pv);
+              w[e] = __uint_as_float(pack_bf16(pv.x, pv.y));
+            }
+            tc::tmem_st32(tS + c * 32, w);
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_full[sb][NT == 1 ? wg : c]);
+          }
+          l_run += lsum.x + lsum.y;
+        }
       }
       if (!ok) break;
 
       // ---- the segment's end: O holds every P V once the last is done
-      {
-        if (!__all_sync(0xffffffffu, mbar_wait(&sh.o_done[s_buffer<NT>(jx - 1, x)],
-                                               s_phase<NT>(jx - 1), &failed))) {
-          ok = false;
-          break;
-        }
-        tc::fence_after_sync();
+      if (!__all_sync(0xffffffffu, mbar_wait_spin(&sh.o_done[s_buffer<NT>(jx - 1, x)],
+                                             s_phase<NT>(jx - 1), &failed))) {
+        ok = false;
+        break;
       }
-      const long long L = (long long)sg.b * p.Hkv * p.MG + sg.vl;
+      tc::fence_after_sync();
       const bool whole = sg.j0 == 0 && sg.j1 == sg.ntiles;
-      const long long slot = L + blockIdx.x;
       const int grow = x * kM + row;  // row within the group
       const long long orow = ((long long)sg.b * p.Hq + (long long)g * p.r) * p.t + rho;
-      __nv_bfloat16 *o = (__nv_bfloat16 *)p.o + orow * D;
-      float *acc = p.acc + (slot * p.group_rows + grow) * D;
-      if (any_of_softmax(found, 128 * nx)) {
+      const int parties = NT == 1 ? 256 : 128 * nx;
+      if (any_of_softmax(found, parties)) {
         if (warp_on)
-          add_unfinite<D>(p, sh, sg, mine, lo, hi, lo0, ncell_tiles, line, orow, m_run, tO);
-        any_of_softmax(false, 128 * nx);  // every row has read the list
+          add_unfinite<D>(p, sh, sg, mine, lo, hi, lo0, ncell_tiles, line, orow, m_run, tO, e0, e0 + NC);
+        any_of_softmax(false, parties);  // every row has read the list
         if (threadIdx.x == 128)
           for (int k = 0; k < kUnfinite; ++k) sh.unfinite[k] = Unfinite{-1, {0u, 0u, 0u, 0u}};
-        any_of_softmax(false, 128 * nx);
+        any_of_softmax(false, parties);
       }
-      if (mine && p.tree && line.depth < 0) {  // padding, or refused: nothing counts
-        m_run = -INFINITY;
-        l_run = 0.f;
+      // NT = 1: the halves swap (m, l); each thread then combines d / 2
+      // columns of both O: o = O_0 a_0 + O_1 a_1, a_h = 2^(m_h - max)
+      float m_all = m_run, l_all = l_run, a0 = 1.f, a1 = 0.f;
+      if constexpr (NT == 1) {
+        // through the unused columns behind P in the last tile's S buffer
+        // (the next segment's first S goes to the other one)
+        const uint32_t tX = tmem + lane_base + s_buffer<NT>(jx - 1, x) * kTile + 32;
+        tmem_st2(tX + wg * 64, m_run, l_run);
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        any_of_softmax(false, parties);
+        tc::fence_after_sync();
+        float m0, l0, m1, l1;
+        tmem_ld2(tX, m0, l0);
+        tmem_ld2(tX + 64, m1, l1);
+        tc::tmem_wait_ld();
+        m_all = fmaxf(m0, m1);
+        // (a half whose scores are all NaN has m = -inf and keeps its NaN sum)
+        a0 = m0 == m_all ? 1.f : exp2f(m0 - m_all);
+        a1 = m1 == m_all ? 1.f : exp2f(m1 - m_all);
+        l_all = l0 * a0 + l1 * a1;
       }
-      const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-      if (warp_on) {
+      if (p.tree && line.depth < 0) {  // padding, or refused: nothing counts
+        m_all = -INFINITY;
+        l_all = 0.f;
+      }
+      // A part that is not the whole group goes to the workspace and is
+      // counted, the early one by warp 3.  A last segment's part whose fellows
+      // have all been counted, before or after its own, needs no merge: this
+      // CTA adds theirs to its O (up to kAddParts of them).
+      constexpr int OC = NT == 1 ? D / 2 : D;  // columns this thread writes
+      const int oc0 = NT == 1 ? wg * OC : 0;
+      const uint32_t tOa = tmem + lane_base + K::TM_O + (NT == 1 ? oc0 : x * D);
+      const Group gr = group_of(p, sg, sh.per);
+      if (p.finish && !whole && sg.j0 == 0 && threadIdx.x == 128)
+        p.splits[blockIdx.x] = make_int2((int)gr.L, gr.np);
+      bool add = false;
+      if (!whole && !is_e && !p.finish && gr.np <= kAddParts) {
+        bool all = false;
+        if (threadIdx.x == 128) all = ld_acquire_gpu(&p.counters[gr.c0]) == gr.np - 1;
+        add = any_of_softmax(all, parties);
+        if (add && threadIdx.x == 128) p.counters[gr.c0] = 0;
+      }
+      if (!whole && !add) {
+        // partials as [column / 4][row][4]: a warp's 32 rows are 512 bytes
+        if (warp_on) {
+          float4 *acc = reinterpret_cast<float4 *>(p.acc) +
+                        ((gr.L + blockIdx.x) * (D / 4) + oc0 / 4) * p.group_rows + grow;
+#pragma unroll 1
+          for (int c = 0; c < OC / 32; ++c) {
+            float ov[32];
+            load_o<D, NT>(tOa + c * 32, a0, a1, l_all == 0.f, ov);
+            if (mine) {
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          float ov[32];
-          tc::tmem_ld32(tO + c * 32, ov);
-          tc::tmem_wait_ld();
-          if (l_run == 0.f) {  // no key at all: zero, whatever the MMA made of it
-#pragma unroll
-            for (int e = 0; e < 32; ++e) ov[e] = 0.f;
+              for (int e = 0; e < 32; e += 4)
+                acc[(long long)(c * 8 + e / 4) * p.group_rows] =
+                    make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+            }
+            __syncwarp();
           }
-          if (mine && whole) {
+          if (mine && (NT == 2 || wg == 0))
+            p.ml[(gr.L + blockIdx.x) * p.group_rows + grow] = make_float2(m_all, l_all);
+          __syncwarp();
+        }
+        if (is_e) {
+          if (lane == 0) mbar_arrive(&sh.early_full);
+        } else if (!p.finish) {
+          any_of_softmax(false, parties);  // the part is written
+          bool last = false;
+          if (threadIdx.x == 128) last = count_part(&p.counters[gr.c0], gr.np);
+          add = any_of_softmax(last, parties);
+          if (add && gr.np > kAddParts) {
+            add = false;
+            left = 1;
+            if (threadIdx.x == 128) sh.late = gr;
+          }
+        }
+      }
+      if ((whole || add) && warp_on) {
+        const float2 *ml = p.ml + (gr.L + gr.c0) * p.group_rows + min(grow, p.group_rows - 1);
+        const int me = (int)blockIdx.x - gr.c0;
+        float m_out = m_all, l_out = l_all;
+        if (add) {  // the exact maximum, then the terms in order
+          float2 y[kAddParts];
+#pragma unroll
+          for (int k = 0; k < kAddParts; ++k)
+            y[k] = k < gr.np && k != me ? __ldcg(&ml[(long long)k * p.group_rows])
+                                        : make_float2(m_all, k == me ? l_all : 0.f);
+#pragma unroll
+          for (int k = 0; k < kAddParts; ++k) m_out = fmaxf(m_out, y[k].x);
+          l_out = 0.f;
+#pragma unroll
+          for (int k = 0; k < kAddParts; ++k) l_out = fmaf(part_weight(y[k], m_out), y[k].y, l_out);
+        }
+        const float inv = l_out == 0.f ? 0.f : 1.f / l_out;  // 0: no key at all
+        __nv_bfloat16 *o = (__nv_bfloat16 *)p.o + orow * D + oc0;
+        const float4 *acc = reinterpret_cast<const float4 *>(p.acc) +
+                            ((gr.L + gr.c0) * (D / 4) + oc0 / 4) * p.group_rows +
+                            min(grow, p.group_rows - 1);
+#pragma unroll 1
+        for (int c = 0; c < OC / 32; ++c) {
+          float ov[32];
+          load_o<D, NT>(tOa + c * 32, a0, a1, l_all == 0.f, ov);
+          if (add) {
+            float a[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) a[e] = 0.f;
+#pragma unroll 1
+            for (int k = 0; k < gr.np; ++k) {
+              if (k == me) {
+                const float w = part_weight(make_float2(m_all, l_all), m_out);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) a[e] = fmaf(w, ov[e], a[e]);
+              } else {
+                float4 v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  v[e] = __ldcg(&acc[((long long)k * (D / 4) + c * 8 + e) * p.group_rows]);
+                const float w = part_weight(__ldcg(&ml[(long long)k * p.group_rows]), m_out);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  a[4 * e] = fmaf(w, v[e].x, a[4 * e]);
+                  a[4 * e + 1] = fmaf(w, v[e].y, a[4 * e + 1]);
+                  a[4 * e + 2] = fmaf(w, v[e].z, a[4 * e + 2]);
+                  a[4 * e + 3] = fmaf(w, v[e].w, a[4 * e + 3]);
+                }
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ov[e] = a[e];
+          }
+          if (mine) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               uint32_t w4[4];
@@ -537,24 +818,50 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
                 w4[k] = pack_bf16(ov[e * 8 + 2 * k] * inv, ov[e * 8 + 2 * k + 1] * inv);
               *reinterpret_cast<uint4 *>(o + c * 32 + e * 8) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
             }
-          } else if (mine) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4 *>(acc + c * 32 + e) = make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
           }
           __syncwarp();
         }
-        if (mine && (!whole || p.scores)) p.ml[slot * p.group_rows + grow] = make_float2(m_run, l_run);
+        if (p.lse && mine && (NT == 2 || wg == 0))
+          p.lse[((long long)sg.b * p.Hkv + g) * p.R + rho] =
+              make_float2(m_out == -INFINITY ? 0.f : m_out, inv);
+        __syncwarp();
       }
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.o_free[x]);
     }
+    // Groups whose last part was counted here and could not be added above
+    // are merged from the workspace, through the rings, which are empty by
+    // now: every tile has been multiplied.  (The first warpgroup takes part in
+    // every segment and speaks for both.)
+    if (any_of_softmax(ok && left, 256, kBarEnd)) merge_group<D>(p, sh.late, smem, warp - 4);
+    Walk begin{sh.b, sh.vl, sh.off, sh.start, sh.end, sh.len};
+    if (begin.next(p, &sg) && is_early(p, sg, true, begin.pos < begin.end)) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&sh.early_done, 0, &failed))) ok = false;
+      if (any_of_softmax(ok && sh.early_last, 256, kBarEnd))
+        merge_group<D>(p, group_of(p, sg, sh.per), smem, warp - 4);
+    }
   } else {
-    if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
     if (warp == 0) {
       // ================================================= TMA producer
       if (lane == 0) {
+        // Q's tiles of the segment.  The first segment's go ahead of its keys;
+        // later ones wait for the buffer (the previous segment's last S), and
+        // their first keys and values do not wait with them.
+        auto load_q = [&](int seg, int nx, int row0, int ln) -> bool {
+          if (seg > 0 && !mbar_wait(&sh.q_empty, (seg - 1) & 1, &failed)) return false;
+          mbar_arrive_expect_tx(&sh.q_full, nx * K::TILE);
+          for (int xx = 0; xx < nx; ++xx)
+#pragma unroll
+            for (int c = 0; c < K::KB; ++c)
+              tc::tma_load_3d(smem + xx * K::TILE + c * K::BLK, &tmQ, c * 64, row0 + xx * kM, ln,
+                              &sh.q_full);
+          return true;
+        };
+        // a single pass over the cache evicts itself first, so that parts and
+        // outputs stay in L2; with several groups per lane others read it too
+        const uint64_t once = p.MG == 1 ? tc::l2_policy_evict_first() : l2_policy_normal();
         int jj = 0, segs = 0, nk = 0, nv = 0;  // tiles, segments, K and V fills so far
         bool ok = true;
         while (ok && walk.next(p, &sg)) {
@@ -562,7 +869,9 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
           const int nx = min(NT, (p.R - grp * p.group_rows + kM - 1) / kM);
           const int ncell_tiles = sg.ntiles - p.tree, lo0 = first_cell(p, sg.n);
           const int ln = sg.b * p.Hkv + g;
-          const int qrow = (sg.b * p.Hq + g * p.r) * p.t + grp * p.group_rows;
+          const int row0 = grp * p.group_rows;
+          if (segs == 0) load_q(segs++, nx, row0, ln);
+          const bool q_due = jj > 0;
           for (int j = sg.j0; ok && j < sg.j1; ++j, ++jj) {
             const int st = jj % K::STAGES;
             const uint32_t par = (jj / K::STAGES - 1) & 1;
@@ -573,25 +882,11 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
               ok = false;
               break;
             }
-            if (j == sg.j0) {
-              // Q's buffer is free once the previous segment's last S is done
-              if (segs > 0 && !mbar_wait(&sh.q_empty, (segs - 1) & 1, &failed)) {
-                ok = false;
-                break;
-              }
-              mbar_arrive_expect_tx(&sh.q_full, nx * K::TILE);
-              for (int xx = 0; xx < nx; ++xx)
-#pragma unroll
-                for (int c = 0; c < K::KB; ++c)
-                  tc::tma_load_2d(smem + xx * K::TILE + c * K::BLK, &tmQ, c * 64, qrow + xx * kM,
-                                  &sh.q_full);
-              ++segs;
-            }
             mbar_arrive_expect_tx(&sh.k_full[st], K::TILE);
 #pragma unroll
             for (int c = 0; c < K::KB; ++c)
-              tc::tma_load_3d(smem + K::OFF_K + st * K::TILE + c * K::BLK, mk, c * 64, c1, ln,
-                              &sh.k_full[st]);
+              tma_load_3d_hint(smem + K::OFF_K + st * K::TILE + c * K::BLK, mk, c * 64, c1, ln,
+                               &sh.k_full[st], once);
             ++nk;
             if (jj >= K::STAGES && !mbar_wait(&sh.v_empty[st], par, &failed)) {
               ok = false;
@@ -600,9 +895,10 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
             mbar_arrive_expect_tx(&sh.v_full[st], K::TILE);
 #pragma unroll
             for (int c = 0; c < K::KB; ++c)
-              tc::tma_load_3d(smem + K::OFF_V + st * K::TILE + c * K::BLK, mv, c * 64, c1, ln,
-                              &sh.v_full[st]);
+              tma_load_3d_hint(smem + K::OFF_V + st * K::TILE + c * K::BLK, mv, c * 64, c1, ln,
+                               &sh.v_full[st], once);
             ++nv;
+            if (j == sg.j0 && q_due && !load_q(segs++, nx, row0, ln)) ok = false;
           }
         }
         // Never leave a copy in flight into an exiting CTA.
@@ -629,17 +925,24 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
           const int st = k % K::STAGES;
           const int sb = s_buffer<NT>(kx, xx);
           if (!mbar_wait(&sh.v_full[st], (k / K::STAGES) & 1, &failed)) return false;
-          if (!mbar_wait(&sh.p_full[sb], s_phase<NT>(kx), &failed)) return false;
           // the previous segment's O has been read out
-          if (first && sx[xx] > 0 && !mbar_wait(&sh.o_free[xx], (sx[xx] - 1) & 1, &failed))
+          if (first && sx[xx] > 0 && !mbar_wait_spin(&sh.o_free[xx], (sx[xx] - 1) & 1, &failed))
             return false;
-          tc::fence_after_sync();
           const uint32_t sV = smem_u32(smem + K::OFF_V + st * K::TILE);
+          // 64 keys at a time, as their P is written: NT = 1 into the half's
+          // own O, NT = 2 both into the row tile's
 #pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            tc::mma_bf16_ts(tmem + K::TM_O + xx * D, tmem + sb * kTile + kk * 8,
-                            tc::sw128_desc(sV + kk * 16 * 128, K::BLK, 1024), idO,
-                            (!first || kk > 0) ? 1u : 0u);
+          for (int h = 0; h < 2; ++h) {
+            if (!mbar_wait_spin(&sh.p_full[sb][h], s_phase<NT>(kx), &failed)) return false;
+            tc::fence_after_sync();
+            // P's first column: over the half's own scores, or behind each other
+            const uint32_t tP = tmem + sb * kTile + h * (NT == 1 ? 64 : 32);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc::mma_bf16_ts(tmem + K::TM_O + (NT == 1 ? h : xx) * D, tP + kk * 8,
+                              tc::sw128_desc(sV + (h * 4 + kk) * 16 * 128, K::BLK, 1024), idO,
+                              (!first || kk > 0 || (NT == 2 && h > 0)) ? 1u : 0u);
+          }
           tc::mma_commit(&sh.o_done[sb]);
           if (last_x) tc::mma_commit(&sh.v_empty[st]);
           return true;
@@ -705,6 +1008,17 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
         uint4 *ob = reinterpret_cast<uint4 *>((__nv_bfloat16 *)p.o + (long long)b * p.Hq * p.t * D);
         for (long long i = lane; i < (long long)p.Hq * p.t * (D / 8); i += 32)
           ob[i] = make_uint4(0, 0, 0, 0);
+      }
+    } else if (lane == 0) {
+      // ================================================= warp 3: the early part
+      if (walk.next(p, &sg) && is_early(p, sg, true, walk.pos < walk.end)) {
+        int last = 0;
+        if (mbar_wait(&sh.early_full, 0, &failed)) {
+          const Group gr = group_of(p, sg, sh.per);
+          last = count_part(&p.counters[gr.c0], gr.np) ? 1 : 0;
+        }
+        sh.early_last = last;
+        mbar_arrive(&sh.early_done);
       }
     }
   }

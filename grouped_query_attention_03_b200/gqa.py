@@ -130,21 +130,31 @@ def _run(dev, what, fn, *args):
     """Call a C entry point with `dev` (the tensors' device) current: the
     library looks up per-device state (SM count, fixed scratch address) on
     the current device."""
-    with torch.cuda.device(dev):
-        _check(fn(*args), what)
+    if dev.index == torch.cuda.current_device():
+        status = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args)
+    if status:
+        raise GQAError(status, what)
+
+
+_DTYPE_CODES = {torch.float32: GQA_F32, torch.bfloat16: GQA_BF16}
 
 
 def _dtype_code(t):
-    if t.dtype == torch.float32:
-        return GQA_F32
-    if t.dtype == torch.bfloat16:
-        return GQA_BF16
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is not None:
+        return code
     raise TypeError(f"unsupported dtype {t.dtype}; use float32 or bfloat16")
 
 
 def _ptr(t, name, dtype=None, device=None):
     if t is None:
         return None
+    if (dtype is not None and device is not None and isinstance(t, torch.Tensor) and
+            t.dtype is dtype and t.is_cuda and t.device == device and t.is_contiguous()):
+        return t.data_ptr()  # the usual case first: a decode step is called often
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -155,12 +165,20 @@ def _ptr(t, name, dtype=None, device=None):
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
+
+
+# The current stream's handle without building a torch.cuda.Stream around it
+# (2 us of a small call), where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream, device):
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _check_lens(lens, B):
@@ -431,7 +449,8 @@ def qk_norm_rope(qkv, Hq, Hkv, d, *, q_weight=None, k_weight=None, eps=1e-6, inv
     if axes is not None:
         if len(axes) != half:
             raise ValueError(f"axes must name the axis of each of the {half} pairs")
-        pair_axis = (ctypes.c_int32 * half)(*axes)
+        if naxes > 1 or any(axes):  # one axis: nothing to say
+            pair_axis = (ctypes.c_int32 * half)(*axes)
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None and w.numel() != d:
             raise ValueError(f"{name} must have {d} elements")
@@ -456,12 +475,13 @@ def qk_norm_rope(qkv, Hq, Hkv, d, *, q_weight=None, k_weight=None, eps=1e-6, inv
 
 
 def decode_tree_workspace(q, k_cache):
-    """A device workspace for decode_tree on these shapes (no initial value;
-    reusable by later calls of any shape that fits)."""
+    """A zero-filled device workspace for decode_tree on these shapes (reusable
+    by later calls of any shape that fits)."""
     B, Hq, t, d = q.shape
     code = _dtype_code(q)
     n = lib().gqa_decode_tree_workspace_bytes(code, B, Hq, k_cache.shape[1], k_cache.shape[2], d, t)
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+    # zero-filled once; every completed call leaves it ready for the next
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=q.device)
 
 
 def decode_tree(q, k_cache, v_cache, k_draft, v_draft, parents, seq_lens, *, window=None,
@@ -531,12 +551,13 @@ def tree_commit(k_cache, v_cache, k_draft, v_draft, path, path_lens, seq_lens, *
 
 
 def decode_scored_workspace(q, k_cache):
-    """A device workspace for decode_scored on these shapes (no initial
-    value; reusable by later calls of any shape that fits)."""
+    """A zero-filled device workspace for decode_scored on these shapes
+    (reusable by later calls of any shape that fits)."""
     B, Hq, t, d = q.shape if q.dim() == 4 else (*q.shape[:2], 1, q.shape[2])
     code = _dtype_code(q)
     n = lib().gqa_decode_scored_workspace_bytes(code, B, Hq, k_cache.shape[1], k_cache.shape[2], d, t)
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+    # zero-filled once; every completed call leaves it ready for the next
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=q.device)
 
 
 def decode_scored(q, k_cache, v_cache, weights, seq_lens, *, scale=None, out=None, workspace=None,

@@ -377,9 +377,12 @@ gqa_status gqa_qk_norm_rope(gqa_dtype dtype, const void *qkv, int64_t batch_stri
  *   o        [B,Hq,t_new,d]
  *   window   as elsewhere, counted in positions: a node at depth m reads
  *            cells >= seq_lens[b] + m - (w - 1) and its last w - 1 ancestors
- *   workspace  gqa_decode_tree_workspace_bytes(...) bytes, 256-byte aligned;
- *            needs no initial value and keeps none.  Calls sharing it must
- *            be ordered
+ *   workspace  gqa_decode_tree_workspace_bytes(...) bytes, 256-byte aligned,
+ *            with gqa_decode's rules: zero-filled once before its first use,
+ *            left ready for the next call of any shape by every call that
+ *            completes, zeroed again after GQA_ERR_TIMEOUT; calls sharing it
+ *            must be ordered.  gqa_decode_tree and gqa_decode_scored may
+ *            share one, not with gqa_decode
  *   dev_status device int32 (required)
  * A length outside [0, C] sets GQA_ERR_CAPACITY and zeroes that sequence's
  * output.  A parent outside [-2, i), or one that is padding or itself
@@ -430,8 +433,8 @@ gqa_status gqa_tree_commit(gqa_dtype dtype, void *k_cache, void *v_cache, const 
  *   weights  device float [B,Hkv,C], in/out; cells >= n_b are left alone
  *   seq_lens device int32 [B], n_b in [t_new, C]
  *   workspace  gqa_decode_scored_workspace_bytes(...) bytes, 256-byte
- *            aligned, no initial value (it holds the scores: 4 bytes per
- *            query row and cell); calls sharing it must be ordered
+ *            aligned, with the rules of gqa_decode_tree's (it holds the
+ *            scores: 4 bytes per query row and cell)
  * A length outside [t_new, C] sets GQA_ERR_CAPACITY, zeroes that sequence's
  * output and leaves its weights.  t_new > GQA_MAX_TREE returns
  * GQA_ERR_UNSUPPORTED.

@@ -315,7 +315,7 @@ def test_a_serving_run(cuda_lib):
     lt = torch.zeros(B, dtype=torch.int32, device=DEV)
     st = cuda_lib.new_status(DEV)
     rot = dict(q_weight=qw, k_weight=qw, inv_freq=fr)
-    ws = torch.empty(32 << 20, dtype=torch.uint8, device=DEV)
+    ws = torch.zeros(32 << 20, dtype=torch.uint8, device=DEV)
     ws1 = torch.zeros(32 << 20, dtype=torch.uint8, device=DEV)
     tree_pos, step_pos = (T + depth).contiguous(), (T + acc)[:, None].contiguous()
     kept = torch.empty(B, Hkv, budget, dtype=torch.int32, device=DEV)

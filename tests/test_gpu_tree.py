@@ -232,11 +232,11 @@ def test_scale_of_either_sign(cuda_lib):
 
 
 def test_one_workspace_many_shapes_streams_and_graphs(cuda_lib):
-    """The workspace needs no initial value; a captured call replays with new
-    inputs in the same buffers; a second stream ordered by events."""
+    """One workspace, zeroed once; a captured call replays with new inputs in
+    the same buffers; a second stream ordered by events."""
     shapes = [(2, 8, 2, 900, 128, 20, [888, 400]), (1, 8, 1, 600, 64, 64, [600]), (1, 4, 4, 300, 128, 3, [5])]
-    ws = torch.full((cuda_lib.lib().gqa_decode_tree_workspace_bytes(1, 2, 8, 2, 900, 128, 128) +
-                     (8 << 20),), 0xff, dtype=torch.uint8, device=DEV)
+    ws = torch.zeros(cuda_lib.lib().gqa_decode_tree_workspace_bytes(1, 2, 8, 2, 900, 128, 128) +
+                     (8 << 20), dtype=torch.uint8, device=DEV)
     side = torch.cuda.Stream()
     for rep in range(2):
         for B, Hq, Hkv, C, d, t, lens in shapes:
