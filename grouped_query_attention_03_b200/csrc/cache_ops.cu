@@ -59,6 +59,44 @@ gqa_status launch_commit(void *kc, void *vc, const void *kd, const void *vd,
                                         st, p));
 }
 
+template <int KPT>
+gqa_status launch_select_k(const gqa::evict::Params &p, int cluster, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)p.B * p.Hkv * cluster));
+  cfg.blockDim = dim3(gqa::evict::kSelThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return launched(cudaLaunchKernelEx(&cfg, gqa::evict::evict_select_kernel<KPT>, p, cluster));
+}
+
+// CTAs per lane: as many as the lanes leave SMs for, up to 8, and as many as
+// its capacity needs to be held in registers (32 keys a thread); a lane that
+// 8 CTAs cannot hold is read again for every digit by one.
+gqa_status launch_select(const gqa::evict::Params &p, int sms, cudaStream_t st) {
+  using namespace gqa::evict;
+  const int64_t lanes = (int64_t)p.B * p.Hkv;
+  const int64_t strips = ((int64_t)p.C + kSelThreads - 1) / kSelThreads;
+  int cluster = 1;
+  while (cluster < kMaxCluster && strips > cluster &&
+         (lanes * cluster * 2 <= 2 * sms || strips > 32 * cluster))
+    cluster *= 2;
+  const int64_t kpt = (strips + cluster - 1) / cluster;
+  if (lanes * cluster > INT_MAX) return GQA_ERR_UNSUPPORTED;
+  if (kpt <= 4) return launch_select_k<4>(p, cluster, st);
+  if (kpt <= 8) return launch_select_k<8>(p, cluster, st);
+  if (kpt <= 16) return launch_select_k<16>(p, cluster, st);
+  if (kpt <= 32) return launch_select_k<32>(p, cluster, st);
+  return launch_select_k<0>(p, 1, st);
+}
+
 template <typename V>
 gqa_status launch_evict_rows(const void *kc, const void *vc, void *ko, void *vo,
                              const gqa::evict::Params &p, int vpr, bool in_place, int sms,
@@ -169,17 +207,7 @@ gqa_status gqa_cache_evict(gqa_dtype dtype, const void *k_cache, const void *v_c
   p.budget = budget;
   p.recent = recent;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const dim3 grid((unsigned)(B * Hkv)), block(gqa::evict::kSelThreads);
-  // Keys in registers up to 32 per thread (the 64 registers that 1024
-  // threads have); fewer when the capacity is small, for fewer compares.
-  cudaError_t e;
-  if (C <= 8 * gqa::evict::kSelThreads)
-    e = gqa::launch_dependent(gqa::evict::evict_select_kernel<8>, grid, block, 0, st, p);
-  else if (C <= 32 * gqa::evict::kSelThreads)
-    e = gqa::launch_dependent(gqa::evict::evict_select_kernel<32>, grid, block, 0, st, p);
-  else
-    e = gqa::launch_dependent(gqa::evict::evict_select_kernel<0>, grid, block, 0, st, p);
-  if ((s = launched(e)) != GQA_OK) return s;
+  if ((s = launch_select(p, di.sms, st)) != GQA_OK) return s;
   const RowVec rv = row_vec(dtype, d, {k_cache, v_cache, k_out, v_out});
   if (rv.bytes == 16)
     return launch_evict_rows<uint4>(k_cache, v_cache, k_out, v_out, p, rv.vpr, in_place, di.sms, st);

@@ -5,20 +5,22 @@
 // weights (equal weights: the lowest cell first).  The survivors keep their
 // order.  Weights compare by value; -0 equals 0 and NaN is below everything.
 //
-// evict_select_kernel, one CTA per lane: the weights become ordered 32-bit
-// keys, held in registers up to 32 per thread (longer lanes read them again
-// from L2).  The k-th largest key T is found digit by digit from the top, 12,
-// 10 and 10 bits: a histogram of the digit over the keys that share T's
-// higher digits, suffix sums over its bins, the bin that holds rank k.  What
-// bounds it is the SM's issue rate, 32768 keys being 1024 warp instructions
-// per step of the loop: three passes of one comparison and few additions
-// where a search by thresholds takes 16 passes of three comparisons each
-// (measured: 8 lanes of 32768 cells 55 us by thresholds of 2 bits).  A warp
-// whose lanes agree on a bin adds them at once, so equal weights (zeros, a
-// fresh cache) do not queue up on one counter.  A pass that finds exactly k
-// keys from T's bin up ends the search.  One prefix sum over (above T, equal
-// to T) places every survivor; the CTA writes the list `kept` and its lane's
-// weights (read completely before, so they may be compacted in place).
+// evict_select_kernel, a cluster of CTAs per lane, each with a run of its
+// cells: the weights become ordered 32-bit keys, held in registers (KPT per
+// thread; lanes too long for that take one CTA that reads them again from
+// L2).  The k-th largest key T is found digit by digit from the top, 11, 11
+// and 10 bits: a histogram of the digit over the keys that share T's higher
+// digits, added up over the cluster through distributed shared memory;
+// suffix sums over its bins and the bin that holds rank k.  A first digit of
+// 11 bits (sign, exponent, two more) tells a few dozen magnitudes apart, so
+// a warp's keys seldom meet on a counter, and usually the second digit ends
+// the search: exactly k keys from T's bin up.  The runs before a CTA's own
+// are counted from the same histograms, so one barrier of the cluster per
+// digit is all that its CTAs wait for.  One prefix sum over (above T, equal
+// to T) places every survivor; the cluster writes the list `kept` and the
+// lane's weights (read completely before, so they may be compacted in
+// place).  Bound by latency: reading the weights, about 2.5 us per digit
+// (counting, cluster barrier, remote counts, scan), placing.
 //
 // Moving the rows (evict_move_kernel) is a gather through `kept`, bound by
 // bandwidth.  Into other caches any order will do: evict_copy_kernel.  In
@@ -35,8 +37,11 @@
 namespace gqa {
 namespace evict {
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
 constexpr int kWarps = kSelThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kBins = 2048;
+constexpr int kPB = kBins / kSelThreads;  // bins per thread
 
 struct Params {
   const float *w;
@@ -58,145 +63,190 @@ __device__ __forceinline__ float key_weight(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
 }
 
-constexpr int kBins = 4096;  // of the first, 12-bit digit
-
-// Finds rank k (from the top, 1-based, at most the total count) among the
-// bins: the bin that holds it, the count above that bin, its own count.
-// Block-wide; BINS is a multiple of kSelThreads.
-template <int BINS>
-__device__ __forceinline__ void find_bin(const uint32_t *hist, uint32_t k, uint32_t *warp_sum,
-                                         uint32_t *result) {
-  constexpr int PER = BINS / kSelThreads;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // thread t has bins [BINS - (t + 1) PER, BINS - t PER), from the top down
-  uint32_t c[PER], sum = 0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    c[i] = hist[BINS - 1 - tid * PER - i];
-    sum += c[i];
-  }
-  uint32_t incl = sum;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += y;
-  }
-  if (lane == 31) warp_sum[warp] = incl;
-  __syncthreads();
-  uint32_t above = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0u);
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    if (above < k && k <= above + c[i]) {  // one thread, one bin
-      result[0] = BINS - 1 - tid * PER - i;
-      result[1] = above;
-      result[2] = c[i];
-    }
-    above += c[i];
-  }
-  __syncthreads();
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Four words of shared memory at the same place in CTA `rank` of the cluster.
+__device__ __forceinline__ uint4 ld_cluster4(const uint32_t *at, uint32_t rank) {
+  uint32_t addr;
+  uint4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(at)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 
-// KPT > 0: lanes of at most KPT * kSelThreads cells, keys in registers;
-// KPT = 0: any length.
+// KPT > 0: a CTA's run is at most KPT * kSelThreads cells, keys in registers;
+// KPT = 0: any length, a cluster of one CTA.
 template <int KPT>
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params p) {
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params p, int cluster) {
   constexpr int STRIPS = KPT > 0 ? KPT : 8;  // strips of kSelThreads cells placed at a time
-  __shared__ uint32_t hist[kBins];
-  __shared__ uint32_t found[3];
+  static_assert(kPB == 4, "a thread's bins are one 16-byte read");
+  __shared__ __align__(16) uint32_t hist[2][kBins];  // [digit & 1], bins from the top down
+  __shared__ uint32_t wtop[kWarps], wbase[kWarps][2], found[3];
   __shared__ uint32_t place[STRIPS * kWarps][2], masks[STRIPS * kWarps][2];
-  __shared__ uint32_t wsum[kWarps][2], wtop[kWarps];
+  __shared__ uint32_t wsum[kWarps][2];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t L = blockIdx.x;
+  const int64_t L = blockIdx.x / cluster;
+  const int rank = (int)(blockIdx.x - L * cluster);
   const int b = (int)(L / p.Hkv);
-  const int n = p.seq_lens[b];
   const float *w = p.w + L * p.C;
   float *wo = p.w_out + L * p.C_out;
   int32_t *kept = p.kept + L * p.budget;
-  if (n < 0 || n > p.C) {
-    if (tid == 0) record_status(p.status, GQA_ERR_CAPACITY);
-    for (int i = tid; i < p.budget; i += kSelThreads) kept[i] = -1;
+  const int t0 = rank * kSelThreads + tid, step = cluster * kSelThreads;
+  // this CTA's cells [r0, r1): whole strips of the capacity, so that the
+  // weights are on their way before the length is known
+  const int run = (p.C + cluster * kSelThreads - 1) / (cluster * kSelThreads) * kSelThreads;
+  const int r0 = min(p.C, rank * run);
+  uint32_t key[STRIPS];
+  if constexpr (KPT > 0) {
+    float x[KPT];
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {
+      const int j = r0 + i * kSelThreads + tid;
+      x[i] = i * kSelThreads < run && j < p.C ? w[j] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) key[i] = order_key(x[i]);
+  }
+  const int n = p.seq_lens[b];
+  if (n < 0 || n > p.C) {  // (the same for the whole cluster)
+    if (t0 == 0) record_status(p.status, GQA_ERR_CAPACITY);
+    for (int i = t0; i < p.budget; i += step) kept[i] = -1;
     return;
   }
   if (n <= p.budget) {  // nothing leaves
-    for (int i = tid; i < p.budget; i += kSelThreads) kept[i] = i < n ? i : -1;
+    for (int i = t0; i < p.budget; i += step) kept[i] = i < n ? i : -1;
     if (wo != w)
-      for (int i = tid; i < n; i += kSelThreads) wo[i] = w[i];
-    for (int i = n + tid; i < p.C_out; i += kSelThreads) wo[i] = 0.f;
+      for (int i = t0; i < n; i += step) wo[i] = w[i];
+    for (int i = n + t0; i < p.C_out; i += step) wo[i] = 0.f;
     return;
   }
-  const int nc = n - p.recent;          // candidates: cells [0, nc)
+  const int nc = n - p.recent;             // candidates: cells [0, nc)
   const uint32_t k = p.budget - p.recent;  // of which the k heaviest stay; k <= nc
-  uint32_t key[STRIPS];
-  if constexpr (KPT > 0) {
-#pragma unroll
-    for (int i = 0; i < KPT; ++i) {
-      const int j = i * kSelThreads + tid;
-      key[i] = j < n ? order_key(w[j]) : 0u;
-    }
-  }
+  const int r1 = min(n, r0 + run);
   // T: the k-th largest candidate key, or after an early end the lower bound
   // of its bin
   uint32_t T = 0, need = 0;  // need: how many of the keys equal to T stay
   bool exact = false;        // every key >= T stays
+  // survivors for sure and keys equal to T in the runs before this one; the
+  // recent cells among them stay
+  uint32_t base_s = max(0, min(r0, n) - nc), base_e = 0;
   if (k > 0) {
-    uint32_t rank = k;  // of T among the keys that share its higher digits
-#pragma unroll
+    uint32_t rank_k = k;  // of T among the keys that share its higher digits
     for (int pass = 0; pass < 3 && !exact; ++pass) {
-      const int shift = pass == 0 ? 20 : (pass == 1 ? 10 : 0);
-      const uint32_t low = pass == 0 ? 4095u : 1023u;
-      const int upper = shift + (pass == 0 ? 12 : 10);  // bits above the digit are T's
-      for (int i = tid; i < (int)low + 1; i += kSelThreads) hist[i] = 0;
+      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+      const uint32_t low = pass < 2 ? 2047u : 1023u;
+      const int above_bits = pass == 0 ? 0 : (pass == 1 ? 21 : 10);  // shift that leaves the higher digits
+      uint32_t *h = hist[pass & 1];
+      *reinterpret_cast<uint4 *>(h + tid * kPB) = make_uint4(0, 0, 0, 0);
       __syncthreads();
       auto count = [&](int j, uint32_t x) {
-        const bool in = j < nc && (pass == 0 || (x >> (upper & 31)) == (T >> (upper & 31)));
-        const uint32_t bin = (x >> shift) & low;
-        const unsigned some = __ballot_sync(0xffffffffu, in);
-        if (some == 0) return;
-        // the lanes that agree with the first counted one go together
-        const int first = __ffs(some) - 1;
-        const uint32_t b0 = __shfl_sync(0xffffffffu, bin, first);
-        const unsigned same = __ballot_sync(0xffffffffu, in && bin == b0);
-        if (lane == first) atomicAdd(&hist[b0], __popc(same));
-        if (in && bin != b0) atomicAdd(&hist[bin], 1u);
+        if (j < r1 && j < nc && (pass == 0 || (x >> above_bits) == (T >> above_bits)))
+          atomicAdd(&h[kBins - 1 - ((x >> shift) & low)], 1u);
       };
       if constexpr (KPT > 0) {
 #pragma unroll
-        for (int i = 0; i < KPT; ++i) count(i * kSelThreads + tid, key[i]);
+        for (int i = 0; i < KPT; ++i) count(r0 + i * kSelThreads + tid, key[i]);
       } else {
-        for (int j0 = 0; j0 < nc; j0 += kSelThreads) {
-          const int j = j0 + tid;
-          count(j, j < nc ? order_key(w[j]) : 0u);
+        for (int j = r0 + tid; j < r1; j += kSelThreads) count(j, order_key(w[j]));
+      }
+      // this thread's four bins: over the cluster, and over the runs before
+      uint4 c, before = make_uint4(0, 0, 0, 0);
+      if (cluster > 1) {
+        // (the others read this histogram until the next digit's barrier, and
+        // the next digit has the other one)
+        cluster_sync();
+        c = make_uint4(0, 0, 0, 0);
+        for (int r = 0; r < cluster; ++r) {
+          if (r == rank) before = c;
+          const uint4 y = ld_cluster4(h + tid * kPB, r);
+          c.x += y.x;
+          c.y += y.y;
+          c.z += y.z;
+          c.w += y.w;
         }
+      } else {
+        __syncthreads();
+        c = *reinterpret_cast<const uint4 *>(h + tid * kPB);
+      }
+      const uint32_t cc[4] = {c.x, c.y, c.z, c.w}, cb[4] = {before.x, before.y, before.z, before.w};
+      const uint32_t sum = c.x + c.y + c.z + c.w;
+      uint32_t incl = sum;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += y;
+      }
+      if (lane == 31) wtop[warp] = incl;
+      __syncthreads();
+      uint32_t above = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? wtop[lane] : 0u);
+      const uint32_t my_above = above;
+#pragma unroll
+      for (int i = 0; i < kPB; ++i) {
+        if (above < rank_k && rank_k <= above + cc[i]) {  // one thread, one bin
+          found[0] = kBins - 1 - (tid * kPB + i);
+          found[1] = above;
+          found[2] = cc[i];
+        }
+        above += cc[i];
       }
       __syncthreads();
-      if (pass == 0)
-        find_bin<4096>(hist, rank, wtop, found);
-      else
-        find_bin<1024>(hist, rank, wtop, found);
       T |= found[0] << shift;
-      rank -= found[1];
-      exact = rank == found[2];
+      const uint32_t up = found[1];
+      exact = rank_k - up == found[2];
+      if (cluster > 1) {
+        // of the runs before: keys in bins above the found one, and in it
+        uint32_t bs = 0, be = 0, at = my_above;
+#pragma unroll
+        for (int i = 0; i < kPB; ++i) {
+          if (at + cc[i] <= up) bs += cb[i];  // above (empty bins hold nothing)
+          if (kBins - 1 - (tid * kPB + i) == (int)found[0]) be = cb[i];
+          at += cc[i];
+        }
+        bs = __reduce_add_sync(0xffffffffu, bs);
+        be = __reduce_add_sync(0xffffffffu, be);
+        if (lane == 0) {
+          wbase[warp][0] = bs;
+          wbase[warp][1] = be;
+        }
+        __syncthreads();
+        base_s += __reduce_add_sync(0xffffffffu, lane < kWarps ? wbase[lane][0] : 0u);
+        base_e = __reduce_add_sync(0xffffffffu, lane < kWarps ? wbase[lane][1] : 0u);
+      }
+      rank_k -= up;
     }
-    need = rank;  // used when not exact: T is then a key, `rank` of its equals stay
+    need = rank_k;  // used when not exact: T is then a key, `need` of its equals stay
+    if (exact) {    // the keys in T's bin stay too
+      base_s += base_e;
+      base_e = 0;
+    }
   }
+  if (cluster > 1) {
+    if (k == 0) cluster_sync();  // every weight of the lane has been read
+    // nobody leaves before all have read its counts: waited for at the end
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  }
+  // does cell j (of key kk) stay for sure, or as one of the equal ones?
+  auto sure_of = [&](int j, uint32_t kk) {
+    return j < r1 && (j >= nc || (k > 0 && (exact ? kk >= T : kk > T)));
+  };
+  auto equal_of = [&](int j, uint32_t kk) { return j < r1 && j < nc && k > 0 && !exact && kk == T; };
   // Place the survivors, STRIPS * kSelThreads cells at a time in ascending
   // order: cell -> strip, warp, lane.
-  uint32_t base_s = 0, base_e = 0;  // survivors for sure, keys equal to T, so far
-  for (int s0 = 0; s0 < n; s0 += STRIPS * kSelThreads) {
+  for (int s0 = r0; s0 < r1; s0 += STRIPS * kSelThreads) {
     if constexpr (KPT == 0) {
 #pragma unroll
       for (int i = 0; i < STRIPS; ++i) {
         const int j = s0 + i * kSelThreads + tid;
-        key[i] = j < n ? order_key(w[j]) : 0u;
+        key[i] = j < r1 ? order_key(w[j]) : 0u;
       }
     }
-    // does cell j (of key kk) stay for sure, or as one of the equal ones?
-    auto sure_of = [&](int j, uint32_t kk) {
-      return j < n && (j >= nc || (k > 0 && (exact ? kk >= T : kk > T)));
-    };
-    auto equal_of = [&](int j, uint32_t kk) { return j < nc && k > 0 && !exact && kk == T; };
 #pragma unroll
     for (int i = 0; i < STRIPS; ++i) {
       const int j = s0 + i * kSelThreads + tid;
@@ -220,9 +270,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params 
     ie = ee;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const uint32_t a = __shfl_up_sync(0xffffffffu, is, off), c = __shfl_up_sync(0xffffffffu, ie, off);
+      const uint32_t x = __shfl_up_sync(0xffffffffu, is, off), c = __shfl_up_sync(0xffffffffu, ie, off);
       if (lane >= off) {
-        is += a;
+        is += x;
         ie += c;
       }
     }
@@ -231,12 +281,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params 
       wsum[warp][1] = ie;
     }
     __syncthreads();
-    uint32_t ws = lane < warp ? wsum[lane][0] : 0u, we = lane < warp ? wsum[lane][1] : 0u;
-    uint32_t ts = wsum[lane][0], te = wsum[lane][1];
-    ws = __reduce_add_sync(0xffffffffu, ws);
-    we = __reduce_add_sync(0xffffffffu, we);
-    ts = __reduce_add_sync(0xffffffffu, ts);
-    te = __reduce_add_sync(0xffffffffu, te);
+    const bool in_w = lane < kWarps;
+    const uint32_t s_l = in_w ? wsum[lane][0] : 0u, e_l = in_w ? wsum[lane][1] : 0u;
+    const uint32_t ws = __reduce_add_sync(0xffffffffu, lane < warp ? s_l : 0u);
+    const uint32_t we = __reduce_add_sync(0xffffffffu, lane < warp ? e_l : 0u);
+    const uint32_t ts = __reduce_add_sync(0xffffffffu, s_l), te = __reduce_add_sync(0xffffffffu, e_l);
     if (tid < STRIPS * kWarps) {
       place[tid][0] = base_s + ws + is - es;
       place[tid][1] = base_e + we + ie - ee;
@@ -253,8 +302,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params 
       if (sure || (eq && e < need)) {
         const uint32_t at = s + min(e, need);
         kept[at] = j;
-        // in place: at <= j, and every weight of this and earlier strips has
-        // been read before the barriers above
+        // in place: at <= j, and every weight up to this strip has been read
+        // before the barriers above (of all runs, with a cluster)
         wo[at] = key_weight(key[i]);
       }
     }
@@ -262,7 +311,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const Params 
     base_e += te;
     __syncthreads();
   }
-  for (int i = p.budget + tid; i < p.C_out; i += kSelThreads) wo[i] = 0.f;
+  for (int i = p.budget + t0; i < p.C_out; i += step) wo[i] = 0.f;
+  if (cluster > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // New lengths, written where the moves are launched (the selection has read

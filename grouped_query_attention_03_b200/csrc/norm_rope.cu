@@ -9,26 +9,29 @@ namespace {
 using namespace gqa::host;
 using gqa::nr::Params;
 
-// Heads per group.  A group computes its token's sines and cosines once for
-// all its heads, so many heads are better -- up to 16, where they cost less
-// than a tenth of the loads and stores -- as long as the grid still fills
-// the GPU twice over; a single token takes one head per group.
-int heads_per_group(int64_t tokens, int heads, int groups_per_cta, int sms) {
-  int hpg = 16;
-  while (hpg > 1 && tokens * ((heads + hpg - 1) / hpg) < (int64_t)2 * sms * groups_per_cta)
-    hpg /= 2;
+// Heads per CTA: all of them (a token's angles are then computed once) as
+// long as that fills every SM four times over, else halved until it does; a
+// few tokens take a head per CTA.
+int heads_per_cta(int64_t token_ctas, int heads, int sms) {
+  int hpg = heads;
+  while (hpg > 1 && token_ctas * ((heads + hpg - 1) / hpg) < (int64_t)4 * sms) hpg = (hpg + 1) / 2;
   return hpg;
 }
 
 template <typename T, int G>
 gqa_status launch_vec(Params p, int sms, cudaStream_t st) {
-  constexpr int per_cta = gqa::nr::kThreads / G;
+  constexpr int tok = gqa::nr::kThreads / G;
   const int heads = p.Hq + 2 * p.Hkv;
-  p.hpg = heads_per_group(p.tokens, heads, per_cta, sms);
-  p.chunks = (heads + p.hpg - 1) / p.hpg;
-  const int64_t grid = (p.tokens * p.chunks + per_cta - 1) / per_cta;
-  if (grid > INT_MAX) return GQA_ERR_UNSUPPORTED;
-  return launched(gqa::launch_dependent(gqa::nr::norm_rope_vec_kernel<T, G>, dim3((unsigned)grid),
+  const int64_t grid = (p.tokens + tok - 1) / tok;
+  p.hpg = heads_per_cta(grid, heads, sms);
+  const int chunks = (heads + p.hpg - 1) / p.hpg;
+  if (grid > INT_MAX || chunks > 65535) return GQA_ERR_UNSUPPORTED;
+  const bool part = 2 * p.half < p.d;
+  auto *kernel = p.interleaved ? (part ? gqa::nr::norm_rope_vec_kernel<T, G, true, true>
+                                       : gqa::nr::norm_rope_vec_kernel<T, G, true, false>)
+                               : (part ? gqa::nr::norm_rope_vec_kernel<T, G, false, true>
+                                       : gqa::nr::norm_rope_vec_kernel<T, G, false, false>);
+  return launched(gqa::launch_dependent(kernel, dim3((unsigned)grid, (unsigned)chunks),
                                         dim3(gqa::nr::kThreads), 0, st, p));
 }
 

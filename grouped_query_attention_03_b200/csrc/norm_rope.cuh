@@ -18,14 +18,17 @@
 // turns, and the top 32 bits go to sincospif as a signed half turn in
 // [-1, 1).
 //
-// Bound by bandwidth: each element read and written once, 8-10 flops.
-// vec kernel: a group of G = 8, 16 or 32 lanes owns a token and a range of
-// heads; a lane holds 16 bytes of a row, so the row's sum of squares and the
-// other half of each pair are a few shuffles away, and each lane's sines
-// and cosines, multiplied into the weights once, serve all its heads.  The
-// groups of a CTA own consecutive tokens: a head's output rows are written
-// as one run.  generic kernel: any width and alignment, a warp per row
-// through shared memory.
+// Each element is read and written once; what stands between that and the
+// memory's rate is instructions, about 60 for the 16 bytes a lane has of a
+// row.  vec kernel: a group of G = 8, 16 or 32 lanes owns a token, the CTA's
+// groups consecutive tokens (a head's output rows are written as one run)
+// and a range of heads, all of them where there are tokens enough.  The
+// CTA first puts its tokens' cosines and sines in shared memory, each
+// computed once; a lane multiplies its own into the weights once for all
+// query heads and once for all key heads, so a row costs a sum of squares,
+// the exchange of the other half of each pair (shuffles) and two packed FMAs
+// per pair of elements.  generic kernel: any width and alignment, a warp per
+// row through shared memory.
 #pragma once
 
 #include "common.cuh"
@@ -35,7 +38,7 @@ namespace nr {
 
 constexpr int kMaxAxes = 4;
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;  // head rows a group has in flight
+constexpr int kUnroll = 4;  // rows a group has in flight
 
 struct Params {
   const void *qkv, *qw, *kw;
@@ -45,7 +48,7 @@ struct Params {
   int64_t batch_stride, row_stride;  // elements
   int64_t tokens;                    // B * T
   int Hq, Hkv, T, d, half, interleaved;
-  int hpg, chunks;  // heads per group, groups per token
+  int hpg;  // heads per CTA
   float eps, inv_d;
   uint32_t axis[8];  // pair i's axis in bits 2 (i % 16) of word i / 16
 };
@@ -69,34 +72,43 @@ __device__ __forceinline__ void angle(const Params &p, int64_t tok, int i, float
   sincospif((float)(int32_t)(frac >> 32) * 4.656612873077393e-10f, sn, cs);  // 2^-31
 }
 
+// A 16-byte vector as fp32 pairs.
 template <typename T>
 struct Vec;
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ void unpack(uint4 u, float *x) {
-    x[0] = bf16lo_to_f32(u.x); x[1] = bf16hi_to_f32(u.x);
-    x[2] = bf16lo_to_f32(u.y); x[3] = bf16hi_to_f32(u.y);
-    x[4] = bf16lo_to_f32(u.z); x[5] = bf16hi_to_f32(u.z);
-    x[6] = bf16lo_to_f32(u.w); x[7] = bf16hi_to_f32(u.w);
+  static __device__ __forceinline__ void unpack(uint4 u, float2 *x) {
+    x[0] = make_float2(bf16lo_to_f32(u.x), bf16hi_to_f32(u.x));
+    x[1] = make_float2(bf16lo_to_f32(u.y), bf16hi_to_f32(u.y));
+    x[2] = make_float2(bf16lo_to_f32(u.z), bf16hi_to_f32(u.z));
+    x[3] = make_float2(bf16lo_to_f32(u.w), bf16hi_to_f32(u.w));
   }
-  static __device__ __forceinline__ uint4 pack(const float *x) {
-    return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                      pack_bf16(x[6], x[7]));
+  static __device__ __forceinline__ uint4 pack(const float2 *x) {
+    return make_uint4(pack_bf16(x[0].x, x[0].y), pack_bf16(x[1].x, x[1].y),
+                      pack_bf16(x[2].x, x[2].y), pack_bf16(x[3].x, x[3].y));
   }
 };
 template <>
 struct Vec<float> {
   static constexpr int N = 4;
-  static __device__ __forceinline__ void unpack(uint4 u, float *x) {
-    x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y);
-    x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
+  static __device__ __forceinline__ void unpack(uint4 u, float2 *x) {
+    x[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+    x[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
   }
-  static __device__ __forceinline__ uint4 pack(const float *x) {
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-                      __float_as_uint(x[3]));
+  static __device__ __forceinline__ uint4 pack(const float2 *x) {
+    return make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x),
+                      __float_as_uint(x[1].y));
   }
 };
+
+__device__ __forceinline__ float2 fmul2v(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+  return *reinterpret_cast<float2 *>(&d);
+}
 
 // 16 bytes, streamed: every row is read once and every output written once.
 __device__ __forceinline__ uint4 ld_stream(const void *p) {
@@ -110,130 +122,147 @@ __device__ __forceinline__ uint4 ld_stream(const void *p) {
 // Rows of d elements as d / N vectors on G lanes (the last lanes idle when
 // d / N is not a power of two).  Needs 16-byte-aligned rows and, for the
 // (i, i + half) pairing, half a multiple of N, so that a lane's partners
-// are the same places of one other lane's vector.
-template <typename T, int G>
-__global__ void __launch_bounds__(kThreads) norm_rope_vec_kernel(const Params p) {
-  constexpr int N = Vec<T>::N;
+// are the same places of one other lane's vector.  INTER: the (2i, 2i + 1)
+// pairing.  PART: some elements are not rotated.
+template <typename T, int G, bool INTER, bool PART>
+__global__ void __launch_bounds__(kThreads, 4) norm_rope_vec_kernel(const Params p) {
+  constexpr int N = Vec<T>::N, H = N / 2, U = kUnroll;
+  constexpr int TOK = kThreads / G;                // tokens per CTA
+  constexpr int MAXHALF = G * N / 2;
+  __shared__ __align__(16) float s_cos[TOK][MAXHALF], s_sin[TOK][MAXHALF];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
-  const int gl = threadIdx.x % G;  // lane of the group
-  const int64_t unit = (int64_t)blockIdx.x * (kThreads / G) + threadIdx.x / G;
-  // every group of the warp takes part in its shuffles, its own unit or not
-  const bool mine = unit < p.tokens * p.chunks;
-  const int64_t tok = mine ? unit % p.tokens : 0;
-  const int chunk = mine ? (int)(unit / p.tokens) : 0;
-  const int64_t b = tok / p.T, t = tok - b * p.T;
+  const int gl = threadIdx.x % G, grp = threadIdx.x / G;
+  const int64_t tok0 = (int64_t)blockIdx.x * TOK, tok = tok0 + grp;
+  const bool mine = tok < p.tokens;
+  const int64_t b = mine ? tok / p.T : 0, t = mine ? tok - b * p.T : 0;
   const int e0 = gl * N;  // first element of this lane
   const bool on = mine && e0 < p.d;
   const int hn = p.Hq + p.Hkv;
-  const int h_first = chunk * p.hpg, h_last = min(h_first + p.hpg, hn + p.Hkv);
+  const int h_first = blockIdx.y * p.hpg, h_last = min(h_first + p.hpg, hn + p.Hkv);
   const T *src = (const T *)p.qkv + b * p.batch_stride + t * p.row_stride + e0;
+  const unsigned full = 0xffffffffu;
 
-  uint4 raw[kUnroll];
+  uint4 raw[U];
+  auto load = [&](int h, int end) {
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u)
-    raw[u] = (on && h_first + u < h_last) ? ld_stream(src + (int64_t)(h_first + u) * p.d)
-                                          : make_uint4(0, 0, 0, 0);
+    for (int u = 0; u < U; ++u)
+      raw[u] = (on && h + u < end) ? ld_stream(src + (int64_t)(h + u) * p.d) : make_uint4(0, 0, 0, 0);
+  };
+  load(h_first, min(h_last, h_first < p.Hq ? p.Hq : hn));
 
-  // this lane's cosines and signed sines, and where its partners are
-  const int hv = p.half / N;  // lanes from one half to the other
-  const bool lowhalf = gl < hv;
-  const int partner =
-      (p.interleaved || gl >= 2 * hv) ? gl : (lowhalf ? gl + hv : gl - hv);
-  float cs[N], sn[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) { cs[i] = 1.f; sn[i] = 0.f; }
-  if (on && h_first < hn) {
-    if (p.interleaved) {
-#pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        if (e0 + i < 2 * p.half) {
-          angle(p, tok, (e0 + i) / 2, &sn[i + 1], &cs[i]);
-          sn[i] = -sn[i + 1];
-          cs[i + 1] = cs[i];
-        }
-      }
-    } else if (gl < 2 * hv) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        angle(p, tok, (lowhalf ? e0 : e0 - p.half) + i, &sn[i], &cs[i]);
-        if (lowhalf) sn[i] = -sn[i];
-      }
+  if (h_first < hn && p.half > 0) {
+    for (int i = threadIdx.x; i < TOK * p.half; i += kThreads) {
+      const int k = i / p.half, pair = i - k * p.half;
+      if (tok0 + k < p.tokens) angle(p, tok0 + k, pair, &s_sin[k][pair], &s_cos[k][pair]);
     }
   }
-  // y_e = r (x_e A_e + x_partner(e) B_e),  A = w cos, B = +-w_partner sin,
-  // r = 1 / sqrt(mean + eps): rebuilt where the heads change from Q to K
-  float A[N], Bc[N];
+  __syncthreads();
+
+  // where this lane's partners are
+  const int hv = p.half / N;  // lanes from one half to the other
+  const bool lowhalf = gl < hv;
+  const int partner = (INTER || gl >= 2 * hv) ? gl : (lowhalf ? gl + hv : gl - hv);
+  // y = r (x A + x_partner B),  A = w cos, B = +-w_partner sin, r = 1 / sqrt(
+  // mean + eps).  Past rot there is no partner (and inf * 0 is not 0).
+  float2 A[H], B[H];
+  bool turned[H];
   auto weigh = [&](const T *w) {
-    const int pe0 = partner * N;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int pe = p.interleaved ? (e0 + (i ^ 1)) : pe0 + i;
-      A[i] = cs[i] * (w && on ? to_f32(w[e0 + i]) : 1.f);
-      Bc[i] = sn[i] * (w && on ? to_f32(w[pe]) : 1.f);
+    for (int i = 0; i < H; ++i) {
+      const int e = e0 + 2 * i;
+      turned[i] = on && e < 2 * p.half;
+      float2 w2 = make_float2(1.f, 1.f), wp = w2;
+      if (w && on) {
+        w2 = make_float2(to_f32(w[e]), to_f32(w[e + 1]));
+        const int pe = partner * N + 2 * i;
+        wp = INTER ? make_float2(w2.y, w2.x) : make_float2(to_f32(w[pe]), to_f32(w[pe + 1]));
+      }
+      A[i] = w2;
+      B[i] = make_float2(0.f, 0.f);
+      if (turned[i]) {
+        if (INTER) {
+          const float c = s_cos[grp][e / 2], n = s_sin[grp][e / 2];
+          A[i] = make_float2(w2.x * c, w2.y * c);
+          B[i] = make_float2(-wp.x * n, wp.y * n);
+        } else {
+          const int pair = lowhalf ? e : e - p.half;
+          const float sg = lowhalf ? -1.f : 1.f;
+          A[i] = make_float2(w2.x * s_cos[grp][pair], w2.y * s_cos[grp][pair + 1]);
+          B[i] = make_float2(sg * wp.x * s_sin[grp][pair], sg * wp.y * s_sin[grp][pair + 1]);
+        }
+      }
     }
   };
-  bool norm = false;
-  const unsigned full = 0xffffffffu;
-  for (int h0 = 0; h0 < p.hpg; h0 += kUnroll) {
-    uint4 next[kUnroll];
+
+  // heads [h, end) of one kind; dst: head h's row of this token
+  auto turn_rows = [&](int h, int end, T *dst, bool norm) {
+    const int64_t step = (int64_t)p.T * p.d;
+    for (; h < end; h += U) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = h_first + h0 + kUnroll + u;
-      next[u] = (on && h0 + kUnroll < p.hpg && h < h_last) ? ld_stream(src + (int64_t)h * p.d)
-                                                           : make_uint4(0, 0, 0, 0);
+      for (int u = 0; u < U; ++u) {
+        if (h + u >= end) break;  // the same for all lanes
+        float2 x[H], xp[H], ss2 = make_float2(0.f, 0.f);
+        Vec<T>::unpack(raw[u], x);
+        float r = 1.f;
+        if (norm) {
+#pragma unroll
+          for (int i = 0; i < H; ++i) ss2 = ffma2v(x[i], x[i], ss2);
+          float ss = ss2.x + ss2.y;
+#pragma unroll
+          for (int off = G / 2; off >= 1; off >>= 1) ss += __shfl_xor_sync(full, ss, off);
+          r = rsqrtf(fmaf(ss, p.inv_d, p.eps));
+        }
+        if (INTER) {
+#pragma unroll
+          for (int i = 0; i < H; ++i) xp[i] = make_float2(x[i].y, x[i].x);
+        } else {
+          uint4 o;
+          o.x = __shfl_sync(full, raw[u].x, partner, G);
+          o.y = __shfl_sync(full, raw[u].y, partner, G);
+          o.z = __shfl_sync(full, raw[u].z, partner, G);
+          o.w = __shfl_sync(full, raw[u].w, partner, G);
+          Vec<T>::unpack(o, xp);
+        }
+        const float2 r2 = make_float2(r, r);
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+          float2 y = fmul2v(x[i], A[i]);
+          if (!PART || turned[i]) y = ffma2v(xp[i], B[i], y);
+          x[i] = fmul2v(y, r2);
+        }
+        if (on) *reinterpret_cast<uint4 *>(dst + u * step) = Vec<T>::pack(x);
+      }
+      dst += U * step;
+      load(h + U, end);
     }
+  };
+  auto row_of = [&](void *out, int heads, int h) {
+    return (T *)out + ((b * heads + h) * p.T + t) * p.d + e0;
+  };
+  int h = h_first;
+  if (h < p.Hq) {
+    const int end = min(h_last, p.Hq);
+    weigh((const T *)p.qw);
+    turn_rows(h, end, row_of(p.q, p.Hq, h), p.qw != nullptr);
+    h = end;
+    load(h, min(h_last, hn));
+  }
+  if (h < h_last && h < hn) {
+    const int end = min(h_last, hn);
+    weigh((const T *)p.kw);
+    turn_rows(h, end, row_of(p.k, p.Hkv, h - p.Hq), p.kw != nullptr);
+    h = end;
+  }
+  if (h < h_last) {  // values: as they are
+    const int64_t step = (int64_t)p.T * p.d;
+    T *dst = row_of(p.v, p.Hkv, h - hn);
+    for (; h < h_last; h += U, dst += U * step) {
+      load(h, h_last);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = h_first + h0 + u;
-      if (h0 + u >= p.hpg) break;  // the same for every lane
-      if ((h0 == 0 && u == 0) || h == p.Hq) {
-        const T *w = (const T *)(h < p.Hq ? p.qw : p.kw);
-        norm = w != nullptr;
-        if (h < hn) weigh(w);
-      }
-      uint4 out = raw[u];
-      // a warp's groups may be at different heads (its tokens wrap into the
-      // next chunk), so the shuffles run for value rows too
-      float x[N], y[N];
-      Vec<T>::unpack(raw[u], x);
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < N; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-      for (int off = G / 2; off >= 1; off >>= 1) ss += __shfl_xor_sync(full, ss, off);
-      float xp[N];
-      if (p.interleaved) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) xp[i] = x[i ^ 1];
-      } else {
-        uint4 o;
-        o.x = __shfl_sync(full, raw[u].x, partner, G);
-        o.y = __shfl_sync(full, raw[u].y, partner, G);
-        o.z = __shfl_sync(full, raw[u].z, partner, G);
-        o.w = __shfl_sync(full, raw[u].w, partner, G);
-        Vec<T>::unpack(o, xp);
-      }
-      if (h < hn) {
-        const float r = norm ? rsqrtf(fmaf(ss, p.inv_d, p.eps)) : 1.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i)  // past rot there is no partner (and inf * 0 is not 0)
-          y[i] = (e0 + i < 2 * p.half ? fmaf(x[i], A[i], xp[i] * Bc[i]) : x[i] * A[i]) * r;
-        out = Vec<T>::pack(y);
-      }
-      if (on && h < h_last) {
-        T *dst;
-        if (h < p.Hq)
-          dst = (T *)p.q + ((b * p.Hq + h) * p.T + t) * p.d;
-        else if (h < hn)
-          dst = (T *)p.k + ((b * p.Hkv + (h - p.Hq)) * p.T + t) * p.d;
-        else
-          dst = (T *)p.v + ((b * p.Hkv + (h - hn)) * p.T + t) * p.d;
-        *reinterpret_cast<uint4 *>(dst + e0) = out;
-      }
+      for (int u = 0; u < U; ++u)
+        if (on && h + u < h_last) *reinterpret_cast<uint4 *>(dst + u * step) = raw[u];
     }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) raw[u] = next[u];
   }
 }
 
