@@ -41,7 +41,7 @@ struct Layout {
   bool scores = false;  // scored: the scores are kept, not multiplied again
   int NT = 1, group_rows = 0, MG = 1, ns = 0, Cp = 0;
   int64_t slots = 0;
-  size_t splits = 0, ml = 0, acc = 0, lse = 0, score_at = 0, total = 0;  // counters at 0
+  size_t groups = 0, ml = 0, acc = 0, lse = 0, score_at = 0, total = 0;  // counters at 0
 };
 
 // Sizes only (no pointers): what gqa_decode_*_workspace_bytes can know.  The
@@ -61,10 +61,10 @@ bool layout(gqa_dtype dtype, int B, int Hq, int Hkv, int C, int d, int t, bool s
     L.MG = (int)((R + 2 * gqa::rows::kM - 1) / (2 * gqa::rows::kM));
     L.group_rows = L.MG == 1 ? (int)R : 2 * gqa::rows::kM;
     L.slots = lanes * L.MG + kMaxCtas;
-    // Parts per lane group if all sequences are of one length, times their
-    // rows: what the last CTA to count would have to read.
+    // Parts per lane group if all sequences are of one length, and their rows:
+    // what the last CTA to count them would have to read.
     const int64_t parts = kMaxCtas / 2 / std::max<int64_t>(lanes * L.MG, 1) + 2;
-    L.finish = parts * L.group_rows > kMergeRows;
+    L.finish = parts > gqa::rows::kAddParts || parts * L.group_rows > kMergeRows;
     L.scores = scored && R <= d / 4;
   } else {
     L.group_rows = gqa::rows::kSR;
@@ -78,8 +78,8 @@ bool layout(gqa_dtype dtype, int B, int Hq, int Hkv, int C, int d, int t, bool s
     L.scores = scored;
   }
   int64_t n;
-  L.splits = round256(gqa::rows::kCounters * sizeof(int));
-  L.ml = L.splits + round256(kMaxCtas * sizeof(int2));
+  L.groups = round256(gqa::rows::kCounters * sizeof(int));
+  L.ml = L.groups + (L.finish ? round256((size_t)(lanes * L.MG) * sizeof(int2)) : 0);
   if (!elems(&n, {L.slots, L.group_rows, 8}) || n > INT64_MAX / 8) return false;
   L.acc = L.ml + round256((size_t)n);
   if (!elems(&n, {L.slots, L.group_rows, (d + 3) / 4, 16}) || n > INT64_MAX / 8) return false;
@@ -206,7 +206,7 @@ gqa_status rows_impl(gqa_dtype dtype, const Operands &op, bool tree, int B, int 
   p.o = op.o;
   p.status = dev_status;
   p.counters = reinterpret_cast<int *>(ws);
-  p.splits = reinterpret_cast<int2 *>(ws + L.splits);
+  p.groups = reinterpret_cast<int2 *>(ws + L.groups);
   p.finish = L.finish ? 1 : 0;
   p.ml = reinterpret_cast<float2 *>(ws + L.ml);
   p.acc = reinterpret_cast<float *>(ws + L.acc);
@@ -231,7 +231,12 @@ gqa_status rows_impl(gqa_dtype dtype, const Operands &op, bool tree, int B, int 
   p.pad = kPadTiles;
   p.ns = L.ns;
   p.scale_log2 = scale * gqa::kLog2e;
-  // the weights' grid, checked before anything is launched
+  // the grids of the kernels that follow, checked before anything is launched
+  const int row_blocks =
+      (std::min(L.group_rows, p.R) + gqa::rows::kFinishRows - 1) / gqa::rows::kFinishRows;
+  const int col_blocks = std::max(1, d / gqa::rows::kFinishCols);
+  const int64_t finish_blocks = (int64_t)B * Hkv * L.MG * row_blocks * col_blocks;
+  if (L.finish && finish_blocks > INT_MAX) return GQA_ERR_UNSUPPORTED;
   const int cell_blocks = (C + gqa::rows::kWeighCells - 1) / gqa::rows::kWeighCells;
   const int64_t grid = tree ? 0 : (int64_t)B * Hkv * cell_blocks;
   if (grid > INT_MAX) return GQA_ERR_UNSUPPORTED;
@@ -246,10 +251,8 @@ gqa_status rows_impl(gqa_dtype dtype, const Operands &op, bool tree, int B, int 
   }
   if (s != GQA_OK) return s;
   if (L.finish) {
-    const int row_blocks = (std::min(L.group_rows, p.R) + gqa::rows::kFinishRows - 1) / gqa::rows::kFinishRows;
-    const int col_blocks = d / gqa::rows::kFinishCols;
     s = launched(gqa::launch_dependent(gqa::rows::rows_finish_kernel<__nv_bfloat16>,
-                                       dim3((unsigned)(p.ctas * row_blocks * col_blocks)),
+                                       dim3((unsigned)finish_blocks),
                                        dim3(gqa::rows::kFinishThreads), 0, st, p, row_blocks, col_blocks));
     if (s != GQA_OK) return s;
   }

@@ -39,8 +39,8 @@ struct Params {
   int32_t *status;
   float2 *ml;               // [slot][group_rows]
   float *acc;               // [slot][ceil(d / 4)][group_rows][4]
-  int2 *splits;             // per CTA: the lane group whose first of several
-                            // parts it has and their number, or -1 (p.finish)
+  int2 *groups;             // [B * Hkv * MG] (p.finish): the CTA of a lane group's
+                            // first part and the number of its parts
   int *counters;            // [kCounters], zero at start and end: parts done
   float2 *lse;              // [B * Hkv][R] (scored): m and 1 / l of every row
   float *scores;            // [B * Hkv][R][Cp] (scored, few rows), else NULL
@@ -239,8 +239,10 @@ __device__ __forceinline__ void merge_parts(const Params &p, long long s0, int n
 }
 
 // ------------------------------------------------------------------- finish
-// Block (CTA of the split, 32 rows, 8 groups of 4 columns): a warp has one
-// group of columns, a lane per row, 8 parts in flight.
+// Block (lane group, 32 rows, 8 groups of 4 columns): a warp has one group of
+// columns, a lane per row.  Up to 16 parts are fetched at once, their
+// statistics and sums together, so that the kernel is two round trips to L2
+// (which group, its parts); more parts take a pass over the statistics first.
 constexpr int kFinishThreads = 256;
 constexpr int kFinishRows = 32, kFinishCols = 32;
 
@@ -254,23 +256,58 @@ __global__ void __launch_bounds__(kFinishThreads)
   int i = blockIdx.x;
   const int cb = i % col_blocks;
   i /= col_blocks;
-  const int rb = i % row_blocks, c = i / row_blocks;
-  const int2 x = p.splits[c];
-  if (x.x < 0) return;
-  const int ln = x.x / p.MG, grp = x.x - ln * p.MG, np = x.y;
+  const int rb = i % row_blocks, L = i / row_blocks;
+  const int2 x = p.groups[L];
+  const int ln = L / p.MG, grp = L - ln * p.MG, np = x.y;
+  if (!length_ok(p, p.seq_lens[ln / p.Hkv])) return;  // (its entry is not written)
+  if (np < 2) return;
   const int rho0 = grp * p.group_rows + rb * kFinishRows;  // first row of the lane
   const int nrows = min(min(kFinishRows, p.group_rows - rb * kFinishRows), p.R - rho0);
   if (nrows <= 0) return;
   const int d4 = p.d / 4, c4 = cb * (kFinishCols / 4) + warp;  // d is 64 or 128
   if (lane < nrows) {
-    const long long s0 = (long long)x.x + c;  // the first part's slot
+    const long long s0 = (long long)L + x.x;  // the first part's slot
     const int row = rb * kFinishRows + lane;
     const float2 *ml = p.ml + s0 * p.group_rows + row;
     const float4 *acc = reinterpret_cast<const float4 *>(p.acc) + s0 * d4 * p.group_rows + row;
-    float m = -INFINITY, l;
-#pragma unroll 8
-    for (int j = 0; j < np; ++j) m = fmaxf(m, ml[(long long)j * p.group_rows].x);
-    merge_columns<1, 8>(p, ml, acc, np, d4, 1, c4, m, &tile[lane][0] - cb * kFinishCols, &l);
+    constexpr int J = 16;
+    const long long step = (long long)d4 * p.group_rows;
+    float2 y[J];
+    float4 v[J];
+    auto fetch = [&](int j0) {
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        if (j0 + j < np) {
+          y[j] = ml[(long long)(j0 + j) * p.group_rows];
+          v[j] = acc[(j0 + j) * step + (long long)c4 * p.group_rows];
+        } else {
+          y[j] = make_float2(-INFINITY, 0.f);
+          v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    };
+    fetch(0);
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < J; ++j) m = fmaxf(m, y[j].x);
+#pragma unroll 16
+    for (int j = J; j < np; ++j) m = fmaxf(m, ml[(long long)j * p.group_rows].x);
+    float l = 0.f, a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+    for (int j0 = 0; j0 < np; j0 += J) {
+      if (j0 > 0) fetch(j0);
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        if (j0 + j >= np) break;
+        const float e = part_weight(y[j], m);
+        l = fmaf(e, y[j].y, l);
+        a0 = fmaf(e, v[j].x, a0);
+        a1 = fmaf(e, v[j].y, a1);
+        a2 = fmaf(e, v[j].z, a2);
+        a3 = fmaf(e, v[j].w, a3);
+      }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // 0: no key at all
+    *reinterpret_cast<float4 *>(&tile[lane][warp * 4]) =
+        make_float4(a0 * inv, a1 * inv, a2 * inv, a3 * inv);
     if (p.lse && c4 == 0)
       p.lse[(long long)ln * p.R + rho0 + lane] =
           make_float2(m == -INFINITY ? 0.f : m, l == 0.f ? 0.f : 1.f / l);
@@ -293,38 +330,54 @@ __global__ void __launch_bounds__(kWeighThreads) rows_weigh_kernel(const Params 
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int ln = blockIdx.x / cell_blocks, part = blockIdx.x - ln * cell_blocks;  // lane (b, g)
-  const int b = ln / p.Hkv, g = ln - b * p.Hkv;
+  const int b = ln / p.Hkv;
+  // cells [j, j + 4) of the lane: the first rows' scores and the weights are
+  // on their way while the length and the rows' statistics are read
+  constexpr int U = 8;
+  const int j = part * kWeighCells + threadIdx.x * 4;
+  const float *s0 = p.scores + (long long)ln * p.R * p.Cp + min(j, p.Cp - 4);
+  float *out = p.weights + (long long)ln * p.C + j;
+  float4 y[U];
+  float old[4];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    y[u] = u < p.R ? *reinterpret_cast<const float4 *>(s0 + (long long)u * p.Cp)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) old[k] = j + k < p.C ? out[k] : 0.f;
   const int n = p.seq_lens[b];
   if (!length_ok(p, n) || part * kWeighCells >= n) return;
-  // weights of cells [j, j + 4) of lane (b, g)
-  const int j = part * kWeighCells + threadIdx.x * 4;
   float w[4] = {0.f, 0.f, 0.f, 0.f};
   for (int r0 = 0; r0 < p.R; r0 += kWeighThreads) {
     const int rho = r0 + threadIdx.x;
     __syncthreads();
     if (rho < p.R) {
-      const float2 y = p.lse[(long long)ln * p.R + rho];
-      s_m[threadIdx.x] = y.x;
-      s_inv[threadIdx.x] = y.y;
+      const float2 x = p.lse[(long long)ln * p.R + rho];
+      s_m[threadIdx.x] = x.x;
+      s_inv[threadIdx.x] = x.y;
     }
     __syncthreads();
-    if (j >= n) continue;
     const int nr = min(kWeighThreads, p.R - r0);
-    const float *s = p.scores + ((long long)(b * p.Hkv + g) * p.R + r0) * p.Cp + j;
-#pragma unroll 4
-    for (int k = 0; k < nr; ++k) {
-      const float4 y = *reinterpret_cast<const float4 *>(s + (long long)k * p.Cp);
-      const float m = s_m[k], inv = s_inv[k];
-      w[0] = fmaf(exp2f(y.x - m), inv, w[0]);
-      w[1] = fmaf(exp2f(y.y - m), inv, w[1]);
-      w[2] = fmaf(exp2f(y.z - m), inv, w[2]);
-      w[3] = fmaf(exp2f(y.w - m), inv, w[3]);
+    for (int k0 = 0; k0 < nr; k0 += U) {
+      if (r0 + k0 > 0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (k0 + u < nr) y[u] = *reinterpret_cast<const float4 *>(s0 + (long long)(r0 + k0 + u) * p.Cp);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (k0 + u >= nr) break;
+        const float m = s_m[k0 + u], inv = s_inv[k0 + u];
+        w[0] = fmaf(exp2f(y[u].x - m), inv, w[0]);
+        w[1] = fmaf(exp2f(y[u].y - m), inv, w[1]);
+        w[2] = fmaf(exp2f(y[u].z - m), inv, w[2]);
+        w[3] = fmaf(exp2f(y[u].w - m), inv, w[3]);
+      }
     }
   }
-  float *out = p.weights + ((long long)b * p.Hkv + g) * p.C + j;
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    if (j + k < n) out[k] += w[k];
+    if (j + k < n) out[k] = old[k] + w[k];
 }
 
 }  // namespace rows

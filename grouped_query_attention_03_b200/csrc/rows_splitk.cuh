@@ -422,7 +422,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         cum += __shfl_sync(0xffffffffu, incl, 31);
       }
     }
-    if (lane == 1 && p.finish) p.splits[blockIdx.x] = make_int2(-1, 0);
     if (lane == 0) {
       sh.b = b;
       sh.vl = vl;
@@ -522,7 +521,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // tiles that some row may not read all of
         const bool edge = draft || c0 + kTile > (p.tree ? sg.n : sg.n - p.t + 1) ||
                           (p.window > 0 && c0 < sg.n + p.t - p.window);
-        if (!__all_sync(0xffffffffu, mbar_wait_spin(&sh.s_full[sb], s_phase<NT>(jx), &failed))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&sh.s_full[sb], s_phase<NT>(jx), &failed))) {
           ok = false;
           break;
         }
@@ -609,7 +608,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             m_run = m_tile;
           } else if (__any_sync(0xffffffffu, m_tile > m_run + kLazyRescale)) {
             // O must hold P V of the previous tile before it is rescaled
-            if (!__all_sync(0xffffffffu, mbar_wait_spin(&sh.o_done[s_buffer<NT>(jx - 1, x)],
+            if (!__all_sync(0xffffffffu, mbar_wait(&sh.o_done[s_buffer<NT>(jx - 1, x)],
                                                    s_phase<NT>(jx - 1), &failed))) {
               ok = false;
               break;
@@ -660,7 +659,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!ok) break;
 
       // ---- the segment's end: O holds every P V once the last is done
-      if (!__all_sync(0xffffffffu, mbar_wait_spin(&sh.o_done[s_buffer<NT>(jx - 1, x)],
+      if (!__all_sync(0xffffffffu, mbar_wait(&sh.o_done[s_buffer<NT>(jx - 1, x)],
                                              s_phase<NT>(jx - 1), &failed))) {
         ok = false;
         break;
@@ -712,8 +711,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int oc0 = NT == 1 ? wg * OC : 0;
       const uint32_t tOa = tmem + lane_base + K::TM_O + (NT == 1 ? oc0 : x * D);
       const Group gr = group_of(p, sg, sh.per);
-      if (p.finish && !whole && sg.j0 == 0 && threadIdx.x == 128)
-        p.splits[blockIdx.x] = make_int2((int)gr.L, gr.np);
+      if (p.finish && sg.j0 == 0 && threadIdx.x == 128) p.groups[gr.L] = make_int2(gr.c0, gr.np);
       bool add = false;
       if (!whole && !is_e && !p.finish && gr.np <= kAddParts) {
         bool all = false;
@@ -926,14 +924,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const int sb = s_buffer<NT>(kx, xx);
           if (!mbar_wait(&sh.v_full[st], (k / K::STAGES) & 1, &failed)) return false;
           // the previous segment's O has been read out
-          if (first && sx[xx] > 0 && !mbar_wait_spin(&sh.o_free[xx], (sx[xx] - 1) & 1, &failed))
+          if (first && sx[xx] > 0 && !mbar_wait(&sh.o_free[xx], (sx[xx] - 1) & 1, &failed))
             return false;
           const uint32_t sV = smem_u32(smem + K::OFF_V + st * K::TILE);
           // 64 keys at a time, as their P is written: NT = 1 into the half's
           // own O, NT = 2 both into the row tile's
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (!mbar_wait_spin(&sh.p_full[sb][h], s_phase<NT>(kx), &failed)) return false;
+            if (!mbar_wait(&sh.p_full[sb][h], s_phase<NT>(kx), &failed)) return false;
             tc::fence_after_sync();
             // P's first column: over the half's own scores, or behind each other
             const uint32_t tP = tmem + sb * kTile + h * (NT == 1 ? 64 : 32);

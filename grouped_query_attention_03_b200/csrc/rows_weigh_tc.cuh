@@ -9,14 +9,15 @@
 // rows on.
 //
 // The product is taken transposed, S^T = K Q^T: a key per TMEM lane, so its
-// sum over the rows stays in one thread (two: 64 rows each), without
-// shuffles or atomics, and every cell belongs to one CTA.  A CTA has a range
-// of (lane, key tile) pairs; a lane's rows are taken 128 at a time, all tiles
-// of its run for each:
+// sum over the rows stays in one thread, without shuffles or atomics, and
+// every cell belongs to one CTA.  A CTA has a range of (lane, key tile)
+// pairs; a lane's rows are taken 128 at a time, all tiles of its run for
+// each:
 //   warp 0     TMA producer: Q tiles (2 buffers), K tiles (ring)
-//   warp 1     tcgen05.mma S^T (M = 128 keys, N = 128 rows, K = d), two
+//   warp 1     tcgen05.mma S^T (M = 128 keys, N = 128 rows, K = d), four
 //              buffers of TMEM
-//   warps 4-11 exponentials and sums; 64 rows per warpgroup
+//   warps 4-11 exponentials and sums; the two warpgroups take the tiles in
+//              turn and never wait for each other within a run
 // Bound by the exponentials: 128 x 128 of them per tile and 128 rows.
 #pragma once
 
@@ -33,21 +34,20 @@ struct WgCfg {
   static constexpr int STAGES = 4;
   static constexpr int OFF_K = 2 * TILE;
   static constexpr int BYTES = OFF_K + STAGES * TILE;
-  // at least 120 KB, so that one CTA (which holds 256 TMEM columns) is alone
-  // on its SM and its loads have the bandwidth
+  // at least 120 KB, so that only one CTA (which holds all 512 TMEM columns)
+  // is resident per SM
   static constexpr int SMEM = (BYTES + 1024 > 120 * 1024 ? BYTES + 1024 : 120 * 1024);
 };
 
 struct WgShared {
-  uint64_t q_full[2], q_empty[2], k_full[4], k_empty[4], s_full[2], s_empty[2], mma_fin;
+  uint64_t q_full[2], q_empty[2], k_full[4], k_empty[4], s_full[4], s_empty[4], mma_fin;
   uint32_t tmem;
   int b, g, tile;
   long long start, end;
   int32_t len[kLenCache];
   // read four at a time
-  alignas(16) float m[2][kM];    // [run & 1]: the 128 rows' statistics
+  alignas(16) float m[2][kM];    // [run & 1]: the 128 rows' -m and 1 / l
   alignas(16) float inv[2][kM];
-  float sum[2][kM];            // [step & 1]: the second warpgroup's sums
 };
 
 // Walks the CTA's range: runs of one lane's tiles.  (Lengths below t hold no
@@ -96,8 +96,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sh.q_full[s], 1);
       mbar_init(&sh.q_empty[s], 1);
+    }
+    for (int s = 0; s < 4; ++s) {
       mbar_init(&sh.s_full[s], 1);
-      mbar_init(&sh.s_empty[s], 8);  // the warps that read S
+      mbar_init(&sh.s_empty[s], 4);  // the warpgroup that reads S
     }
     for (int s = 0; s < K::STAGES; ++s) {
       mbar_init(&sh.k_full[s], 1);
@@ -107,7 +109,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) {
-    tc::tmem_alloc(&sh.tmem, 256);
+    tc::tmem_alloc(&sh.tmem, 512);
     tc::tmem_relinquish();
   }
   if (warp == 0 && lane == 0) {
@@ -173,8 +175,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp >= 4) {
     const int wg = (warp - 4) >> 2, q4 = warp & 3;
     const int key = q4 * 32 + lane;  // within the tile
-    const uint32_t tS0 = tmem + ((uint32_t)(q4 * 32) << 16) + wg * 64;
+    const uint32_t tS0 = tmem + ((uint32_t)(q4 * 32) << 16);
     const float sc = p.scale_log2 == 0.f ? 1e-30f : p.scale_log2;
+    const float masked = sc < 0.f ? INFINITY : -INFINITY;  // 2^(sc masked) = 0
     int step = 0, run = 0;
     bool ok = true;
     while (ok && walk.next(p, &b, &g, &n, &j0, &j1)) {
@@ -183,57 +186,60 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int q = 0; ok && q < MQ; ++q, ++run) {
         const int rb = run & 1;
         // the rows' statistics (rows past the lane's: weight 0).  Written by
-        // the threads of the first warpgroup; the buffer's last readers
-        // passed the barrier of the run between.
+        // the first warpgroup; the buffer's last readers have passed the
+        // barrier of the run between.
         if (wg == 0) {
           const int rho = q * kM + key;
           const float2 y = rho < p.R ? p.lse[ln * p.R + rho] : make_float2(0.f, 0.f);
-          sh.m[rb][key] = y.x;
+          sh.m[rb][key] = -y.x;
           sh.inv[rb][key] = y.y;
         }
         any_of_softmax(false, 256);
         for (int j = j0; j < j1; ++j, ++step) {
-          const int sb = step & 1;
-          if (!__all_sync(0xffffffffu, mbar_wait_spin(&sh.s_full[sb], (step >> 1) & 1, &failed))) {
+          if ((step & 1) != wg) continue;
+          const int sb = step & 3;
+          const int cell = j * kTile + key;
+          const float old = cell < n ? w[cell] : 0.f;  // one thread per run; a barrier between runs
+          if (!__all_sync(0xffffffffu, mbar_wait(&sh.s_full[sb], (step >> 2) & 1, &failed))) {
             ok = false;
             break;
           }
           tc::fence_after_sync();
-          float s[64];
-          tc::tmem_ld32(tS0 + sb * kTile, s);
-          tc::tmem_ld32(tS0 + sb * kTile + 32, s + 32);
-          tc::tmem_wait_ld();
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.s_empty[sb]);
-          const int cell = j * kTile + key;
-          const float4 *m4 = reinterpret_cast<const float4 *>(&sh.m[rb][wg * 64]);
-          const float4 *i4 = reinterpret_cast<const float4 *>(&sh.inv[rb][wg * 64]);
-          float sum0 = 0.f, sum1 = 0.f;
-          if ((j + 1) * kTile > n - p.t + 1) {  // some row may not read all of the tile
-            int i = (q * kM + wg * 64) % p.t;
-            const int behind = cell - (n - p.t);  // row i reads the cell if i >= behind
+          const bool edge = (j + 1) * kTile > n - p.t + 1;  // some row may not read all of it
+          const int behind = cell - (n - p.t);              // row i reads the cell if i >= behind
+          const float2 sc2 = make_float2(sc, sc);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          int i = (q * kM) % p.t;
 #pragma unroll
-            for (int e = 0; e < 64; ++e) {
-              const float m = sh.m[rb][wg * 64 + e], inv = sh.inv[rb][wg * 64 + e];
-              if (i >= behind) sum0 = fmaf(ex2_approx(fmaf(s[e], sc, -m)), inv, sum0);
-              if (++i == p.t) i = 0;
+          for (int half = 0; half < 2; ++half) {
+            float s[64];
+            tc::tmem_ld32(tS0 + sb * kTile + half * 64, s);
+            tc::tmem_ld32(tS0 + sb * kTile + half * 64 + 32, s + 32);
+            tc::tmem_wait_ld();
+            if (half == 1) {
+              tc::fence_before_sync();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sh.s_empty[sb]);
             }
-          } else {
+            const float4 *m4 = reinterpret_cast<const float4 *>(&sh.m[rb][half * 64]);
+            const float4 *i4 = reinterpret_cast<const float4 *>(&sh.inv[rb][half * 64]);
+            if (edge) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float4 m = m4[e], inv = i4[e];
-              sum0 = fmaf(ex2_approx(fmaf(s[4 * e], sc, -m.x)), inv.x, sum0);
-              sum1 = fmaf(ex2_approx(fmaf(s[4 * e + 1], sc, -m.y)), inv.y, sum1);
-              sum0 = fmaf(ex2_approx(fmaf(s[4 * e + 2], sc, -m.z)), inv.z, sum0);
-              sum1 = fmaf(ex2_approx(fmaf(s[4 * e + 3], sc, -m.w)), inv.w, sum1);
+              for (int e = 0; e < 64; ++e) {
+                if (i < behind) s[e] = masked;
+                if (++i == p.t) i = 0;
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 64; e += 4) {
+              const float4 m = m4[e / 4], inv = i4[e / 4];
+              const float2 x = ffma2v(make_float2(s[e], s[e + 1]), sc2, make_float2(m.x, m.y));
+              const float2 y = ffma2v(make_float2(s[e + 2], s[e + 3]), sc2, make_float2(m.z, m.w));
+              sum[0] = ffma2v(make_float2(ex2_approx(x.x), ex2_approx(x.y)), make_float2(inv.x, inv.y), sum[0]);
+              sum[1] = ffma2v(make_float2(ex2_approx(y.x), ex2_approx(y.y)), make_float2(inv.z, inv.w), sum[1]);
             }
           }
-          // the second warpgroup's rows join the first's (one barrier a step:
-          // the buffer is written again two steps later, behind the next)
-          if (wg == 1) sh.sum[sb][key] = sum0 + sum1;
-          any_of_softmax(false, 256);
-          if (wg == 0 && cell < n) w[cell] += (sum0 + sum1) + sh.sum[sb][key];
+          if (cell < n) w[cell] = old + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
         }
       }
     }
@@ -289,9 +295,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             break;
           }
           for (int j = j0; j < j1; ++j, ++step) {
-            const int st = step % K::STAGES, sb = step & 1;
+            const int st = step % K::STAGES, sb = step & 3;
             if (!mbar_wait(&sh.k_full[st], (step / K::STAGES) & 1, &failed) ||
-                (step >= 2 && !mbar_wait_spin(&sh.s_empty[sb], ((step >> 1) - 1) & 1, &failed))) {
+                (step >= 4 && !mbar_wait(&sh.s_empty[sb], ((step >> 2) - 1) & 1, &failed))) {
               ok = false;
               break;
             }
@@ -319,7 +325,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == 1) tc::tmem_dealloc(tmem, 256);
+  if (warp == 1) tc::tmem_dealloc(tmem, 512);
 }
 
 }  // namespace rows

@@ -152,9 +152,11 @@ def _dtype_code(t):
 def _ptr(t, name, dtype=None, device=None):
     if t is None:
         return None
-    if (dtype is not None and device is not None and isinstance(t, torch.Tensor) and
-            t.dtype is dtype and t.is_cuda and t.device == device and t.is_contiguous()):
-        return t.data_ptr()  # the usual case first: a decode step is called often
+    try:  # the usual case first: a decode step is called often
+        if t.dtype is dtype and t.get_device() == device.index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # not a tensor, or no device given
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
