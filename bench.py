@@ -167,20 +167,20 @@ def pass_stats(ms):
 # lines stripped: once the code changes the figure no longer describes the
 # kernel and is reported as null (a comment edit does not count).
 DECODE_SOURCES = ["decode_splitk.cuh", "common.cuh", "tc_ptx.cuh"]
-DECODE_SHA = "f5815f28d2eec9e95b0d4534fc3a003f3b7bcf1c684160196fa61561e521d95b"
+DECODE_SHA = "208de03d72f85999121694dd9b1be4a5a8935ee7154e41f2331910dd359a4f16"
 PAIR_SOURCES = ["prefill_pair.cuh", "common.cuh", "tc_ptx.cuh"]
 PAIR_SHA = "b55fbb607750b596aa7e864859eb103b7cdf4955fb5bdd52daec85227937995e"
 PERSIST_SOURCES = ["prefill_persist.cuh", "common.cuh", "tc_ptx.cuh"]
 PERSIST_SHA = "914d32926d329e3c21c2ce75b7f79d52bc53e403126ff2afbf4fb0ab7a1907b0"
 CAPTURED_TRAFFIC = [
     {"workload": "decode_b8_n8000", "phase": "decode", "window": None, "hkv": None,
-     "bytes": 268_040_448, "sources": DECODE_SOURCES, "sha256": DECODE_SHA},
+     "bytes": 267_731_712, "sources": DECODE_SOURCES, "sha256": DECODE_SHA},
     {"workload": "decode_ragged", "phase": "decode", "window": None, "hkv": 1,
-     "bytes": 148_212_992, "sources": DECODE_SOURCES, "sha256": DECODE_SHA},
+     "bytes": 147_660_800, "sources": DECODE_SOURCES, "sha256": DECODE_SHA},
     {"workload": "decode_ragged", "phase": "decode", "window": None, "hkv": 8,
-     "bytes": 1_125_684_880, "sources": DECODE_SOURCES, "sha256": DECODE_SHA},
+     "bytes": 1_124_573_952, "sources": DECODE_SOURCES, "sha256": DECODE_SHA},
     {"workload": "swa_t32768", "phase": "decode", "window": None, "hkv": None,
-     "bytes": 17_117_952, "sources": DECODE_SOURCES, "sha256": DECODE_SHA},
+     "bytes": 17_116_160, "sources": DECODE_SOURCES, "sha256": DECODE_SHA},
     {"workload": "prefill_b4_t1024", "phase": "prefill", "window": None, "hkv": None,
      "bytes": 6_359_808, "sources": PERSIST_SOURCES, "sha256": PERSIST_SHA},
     {"workload": "prefill_b4_t1024", "phase": "prefill", "window": 256, "hkv": None,

@@ -50,6 +50,12 @@
 // range (planned from the lengths as they read then) while that kernel
 // drains, then waits for it to complete (griddepcontrol.wait) before it
 // reads anything it uses or writes anything.
+//
+// SC (gqa_decode_scored, one row): every scaled score also goes to the
+// workspace and each head's merged maximum and 1 / sum beside it, from which
+// another kernel adds up what each cell received.  The sum is then of the
+// fp32 weights (2^-9 of a rounded one would show in fp32 results), and a
+// refused length empties its own sequence only.
 #pragma once
 
 #include <cuda.h>
@@ -154,11 +160,17 @@ struct Params {
   int ring;       // 1: the cache is a rolling buffer of C slots, position p
                   // in slot p mod C; the query reads all min(n_b, C) slots
   int pad;        // virtual rows in front of every non-empty lane (below)
+  // SC: scores [B * Hkv][r][Cp] and (m, 1 / l) [B * Hkv][r]
+  float *scores;
+  float2 *lse;
+  int Cp;
 };
 
 // Keys of sequence b for this call (n_b, the appended token included).
+template <bool SC = false>
 __device__ __forceinline__ int nlen(const Params &p, int b) {
-  return p.seq_lens[b] + p.add;
+  const int n = p.seq_lens[b] + p.add;
+  return SC && n > p.C ? 0 : n;  // (SC: refused like one below 1)
 }
 
 // a / b for non-negative a and positive b, with the 32-bit divide when
@@ -210,7 +222,7 @@ constexpr int kPrefetchRows = 512;
 // are read through L2 only (ld.global.cg), so no line of them sits in this
 // SM's L1 when the producer reads them after the wait.  Invalid lengths,
 // or more sequences than the shared cache holds, prefetch nothing.
-template <int D, int R>
+template <int D, int R, bool SC>
 __device__ void prefetch_range(const Params &p, const CUtensorMap *tmK,
                                const CUtensorMap *tmV, int *s_len) {
   using K = Cfg<D, R>;
@@ -220,7 +232,8 @@ __device__ void prefetch_range(const Params &p, const CUtensorMap *tmK,
   long long tot = 0;
   int bad_local = 0;
   for (int b = lane; b < p.B; b += 32) {
-    const int n = __ldcg(p.seq_lens + b) + p.add;
+    int n = __ldcg(p.seq_lens + b) + p.add;
+    if (SC && (n < 0 || n > p.C)) n = 0;
     s_len[b] = n;
     bad_local |= (n < p.add || (!p.ring && n > p.C));
     tot += extent(p, eligible_cells(p, max(n, 0)));
@@ -312,7 +325,7 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
 }
 
 // -------------------------------------------------------------- producer
-template <int D, int R>
+template <int D, int R, bool SC>
 __device__ void producer(const Params &p, const CUtensorMap *tmK,
                          const CUtensorMap *tmV, unsigned char *smem,
                          StageHdr *hdrs, uint64_t *full, uint64_t *empty,
@@ -344,16 +357,22 @@ __device__ void producer(const Params &p, const CUtensorMap *tmK,
   long long tot = 0;
   int bad_local = 0;
   for (int b = lane; b < p.B; b += 32) {
-    const int n = nlen(p, b);
+    const int n = SC ? max(nlen<SC>(p, b), 0) : nlen(p, b);
     if (p.lens_smem) s_len[b] = n;
-    bad_local |= (n < p.add || (!p.ring && n > p.C));
+    if (SC) {
+      if (n == 0) record_status(p.status, GQA_ERR_CAPACITY);
+    } else {
+      bad_local |= (n < p.add || (!p.ring && n > p.C));
+    }
     tot += extent(p, eligible_cells(p, max(n, 0)));
   }
   const bool bad = __any_sync(0xffffffffu, bad_local) != 0;
   if (lane == 0) *s_bad = bad ? 1 : 0;
   __syncwarp();
   mbar_arrive(lens_ready);
-  auto len_of = [&](int bb) { return p.lens_smem ? s_len[bb] : nlen(p, bb); };
+  auto len_of = [&](int bb) {
+    return p.lens_smem ? s_len[bb] : (SC ? max(nlen<SC>(p, bb), 0) : nlen(p, bb));
+  };
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1)
     tot += __shfl_xor_sync(0xffffffffu, tot, off);
@@ -525,7 +544,8 @@ __device__ __forceinline__ void fence_acq_rel_gpu() {
 // (the partials were just written by other CTAs).
 template <int D, int R, int NT>
 __device__ __noinline__ void merge_lane(const Params &p, int L, int c0, int np,
-                                        __nv_bfloat16 *out, int rc, int t) {
+                                        __nv_bfloat16 *out, int rc, int t,
+                                        float2 *lse = nullptr) {
   constexpr int G4 = R * D / 4;                 // float4 groups of one partial
   constexpr int QPT = (G4 + NT - 1) / NT;       // groups per thread
   constexpr int NB = QPT == 1 ? 16 : (QPT == 2 ? 8 : (QPT <= 4 ? 4 : 2));  // per batch
@@ -610,8 +630,15 @@ __device__ __noinline__ void merge_lane(const Params &p, int L, int c0, int np,
       const float inv = 1.f / l[i];
       *reinterpret_cast<uint2 *>(out + q4 * 4) =
           make_uint2(pack_bf16(x[i][0] * inv, x[i][1] * inv), pack_bf16(x[i][2] * inv, x[i][3] * inv));
+      if (lse && q4 % (D / 4) == 0) lse[hq[i]] = make_float2(m[i], inv);
     }
   }
+}
+
+// Virtual lane L's first head in the statistics (SC).
+__device__ __forceinline__ float2 *lse_of(const Params &p, int L, int R) {
+  const int b = L / p.VL, vl = L % p.VL;
+  return p.lse + ((size_t)b * p.Hkv + vl / p.nsub) * p.r + (vl % p.nsub) * R;
 }
 
 // ------------------------------------------------------------- consumers
@@ -621,7 +648,7 @@ __device__ __noinline__ void merge_lane(const Params &p, int L, int c0, int np,
 //   B regs 0..1: (rows 2t..2t+1, col g), (rows 8+2t.., col g)
 //   C regs 0..3: (row g, cols 2t, 2t+1), (row g+8, cols 2t, 2t+1)
 // Tile rows are query heads; S columns are cache rows; O columns features.
-template <int D, int R>
+template <int D, int R, bool SC>
 __device__ void consumer(const Params &p, unsigned char *smem,
                          const StageHdr *hdrs, uint64_t *full, uint64_t *empty,
                          uint64_t *comb, int &merge_flag) {
@@ -738,6 +765,15 @@ __device__ void consumer(const Params &p, unsigned char *smem,
           const float v = s[e] + s2[e];
           s[e] = (e < 2 ? r0 : r1) ? v * p.scale_log2 : -INFINITY;
         }
+        if constexpr (SC) {
+          const int vl = hd.lane % p.VL, h0 = (vl % p.nsub) * R, rc = min(R, p.r - h0);
+          const size_t kv = (size_t)(hd.lane / p.VL) * p.Hkv + vl / p.nsub;
+          float *at = p.scores + (kv * p.r + h0) * p.Cp + hd.cell0 + w * kBR + g;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if ((e < 2 ? r0 : r1) && 2 * t + (e & 1) < rc)
+              at[(size_t)(2 * t + (e & 1)) * p.Cp + (e < 2 ? 0 : 8)] = s[e];
+        }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           float mx = fmaxf(s[j], s[j + 2]);
@@ -764,8 +800,13 @@ __device__ void consumer(const Params &p, unsigned char *smem,
         const uint32_t p0 = pack_bf16(pv[0], pv[1]);  // row g: heads 2t, 2t + 1
         const uint32_t p1 = pack_bf16(pv[2], pv[3]);  // row g + 8
         // the denominator sums exactly the bf16 weights the MMA uses
-        l_run[0] += bf16lo_to_f32(p0) + bf16lo_to_f32(p1);
-        l_run[1] += bf16hi_to_f32(p0) + bf16hi_to_f32(p1);
+        if constexpr (SC) {
+          l_run[0] += pv[0] + pv[2];
+          l_run[1] += pv[1] + pv[3];
+        } else {
+          l_run[0] += bf16lo_to_f32(p0) + bf16lo_to_f32(p1);
+          l_run[1] += bf16hi_to_f32(p0) + bf16hi_to_f32(p1);
+        }
         // P^T as the B operand: rows 2t, 2t + 1 (and + 8) of head column g
         const uint32_t pb0 = movmatrix_t(p0), pb1 = movmatrix_t(p1);
         // ---- O^T += V^T P^T (A = V^T by transposing loads, 16 features a tile)
@@ -806,6 +847,18 @@ __device__ void consumer(const Params &p, unsigned char *smem,
             s[nt][e] = v;
             mx[e >> 1] = fmaxf(mx[e >> 1], v);
           }
+        if constexpr (SC) {
+          const int vl = hd.lane % p.VL, h0 = (vl % p.nsub) * R, rc = min(R, p.r - h0);
+          const size_t kv = (size_t)(hd.lane / p.VL) * p.Hkv + vl / p.nsub;
+          float *at = p.scores + (kv * p.r + h0) * p.Cp + hd.cell0 + w * kBR;
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int col = nt * 8 + 2 * t + (e & 1), head = g + (e >> 1) * 8;
+              if (col < nv && head < rc) at[(size_t)head * p.Cp + col] = s[nt][e];
+            }
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
@@ -833,8 +886,13 @@ __device__ void consumer(const Params &p, unsigned char *smem,
           pa[2 * nt] = pack_bf16(pv[0], pv[1]);
           pa[2 * nt + 1] = pack_bf16(pv[2], pv[3]);
           // the denominator sums exactly the bf16 weights the MMA uses
-          l_run[0] += bf16lo_to_f32(pa[2 * nt]) + bf16hi_to_f32(pa[2 * nt]);
-          l_run[1] += bf16lo_to_f32(pa[2 * nt + 1]) + bf16hi_to_f32(pa[2 * nt + 1]);
+          if constexpr (SC) {
+            l_run[0] += pv[0] + pv[1];
+            l_run[1] += pv[2] + pv[3];
+          } else {
+            l_run[0] += bf16lo_to_f32(pa[2 * nt]) + bf16hi_to_f32(pa[2 * nt]);
+            l_run[1] += bf16lo_to_f32(pa[2 * nt + 1]) + bf16hi_to_f32(pa[2 * nt + 1]);
+          }
         }
         // ---- O += P V (A = P over the 16 cache rows, B = V rows from smem)
         const int vrow = w * kBR + (lane & 7) + ((lane >> 3) & 1) * 8;
@@ -942,6 +1000,7 @@ __device__ void consumer(const Params &p, unsigned char *smem,
 #pragma unroll
             for (int k = 0; k < D / 32; ++k)
               out[h * D + lane + 32 * k] = __float2bfloat16_rn(a[k] * inv);
+            if (SC && lane == 0) lse_of(p, L, R)[h] = make_float2(mm, inv);
           }
         } else {
           // The lane's merge reads this partial at the end of the kernel,
@@ -1002,18 +1061,19 @@ __device__ void consumer(const Params &p, unsigned char *smem,
       const int h0 = (vl / p.nsub) * p.r + (vl % p.nsub) * R;
       const int rc = min(R, p.r - (vl % p.nsub) * R);
       __nv_bfloat16 *out = p.o + ((size_t)b * p.Hq + h0) * D;
+      float2 *lse = SC ? lse_of(p, L, R) : nullptr;
       if (flags != 3)
-        merge_lane<D, R, NWC * 32>(p, L, i ? pc1 : pc0, i ? pn1 : pn0, out, rc, threadIdx.x);
+        merge_lane<D, R, NWC * 32>(p, L, i ? pc1 : pc0, i ? pn1 : pn0, out, rc, threadIdx.x, lse);
       else if (w < 4)
-        merge_lane<D, R, NA>(p, L, pc0, pn0, out, rc, threadIdx.x);
+        merge_lane<D, R, NA>(p, L, pc0, pn0, out, rc, threadIdx.x, lse);
       else
-        merge_lane<D, R, NBT>(p, L, pc1, pn1, out, rc, threadIdx.x - NA);
+        merge_lane<D, R, NBT>(p, L, pc1, pn1, out, rc, threadIdx.x - NA, lse);
     }
   }
   if (failed && lane == 0) record_status(p.status, kStatusTimeout);
 }
 
-template <int D, int R>
+template <int D, int R, bool SC = false>
 __global__ void __launch_bounds__(Cfg<D, R>::THREADS, Cfg<D, R>::MIN_BLOCKS)
     split_kernel(const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, const Params p) {
@@ -1049,11 +1109,11 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, Cfg<D, R>::MIN_BLOCKS)
   // kernel on the stream may use: wait until it has completed (a no-op when
   // the launch is not a programmatic dependent), then let the next kernel
   // start its own set-up.
-  if (warp == K::NWC) prefetch_range<D, R>(p, &tmK, &tmV, s_len);
+  if (warp == K::NWC) prefetch_range<D, R, SC>(p, &tmK, &tmV, s_len);
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   if (warp == K::NWC) {
-    producer<D, R>(p, &tmK, &tmV, smem, hdrs, full, empty, s_len, &s_bad, &lens_ready);
+    producer<D, R, SC>(p, &tmK, &tmV, smem, hdrs, full, empty, s_len, &s_bad, &lens_ready);
   } else {
     // The producer validates every length (each must give n_b in [0, C];
     // otherwise the call writes only zeros) and caches them.
@@ -1084,12 +1144,12 @@ __global__ void __launch_bounds__(Cfg<D, R>::THREADS, Cfg<D, R>::MIN_BLOCKS)
     // Rows of sequences with nothing to attend to (n_b = 0, or any invalid
     // length) are zeros; CTA c takes batch rows c, c + G, ...
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-      if (!bad && (p.lens_smem ? s_len[b] : nlen(p, b)) > 0) continue;
+      if (!bad && (p.lens_smem ? s_len[b] : nlen<SC>(p, b)) > 0) continue;
       __nv_bfloat16 *ob = p.o + (size_t)b * p.Hq * D;
       for (int i = threadIdx.x; i < p.Hq * D / 8; i += K::NWC * 32)
         reinterpret_cast<uint4 *>(ob)[i] = make_uint4(0, 0, 0, 0);
     }
-    consumer<D, R>(p, smem, hdrs, full, empty, &comb, merge_flag);
+    consumer<D, R, SC>(p, smem, hdrs, full, empty, &comb, merge_flag);
   }
 }
 

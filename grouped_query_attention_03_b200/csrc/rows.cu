@@ -2,6 +2,7 @@
 // workspace, the choice of kernel, launches.
 #include <algorithm>
 
+#include "decode_host.cuh"
 #include "host.cuh"
 #include "rows_simt.cuh"
 #include "rows_splitk.cuh"
@@ -37,6 +38,7 @@ constexpr int kMergeRows = GQA_ROWS_MERGE;
 
 struct Layout {
   bool tc = false;
+  bool dec = false;     // scored, one row: the decode kernel
   bool finish = false;  // the parts are merged by a kernel of their own
   bool scores = false;  // scored: the scores are kept, not multiplied again
   int NT = 1, group_rows = 0, MG = 1, ns = 0, Cp = 0;
@@ -54,7 +56,18 @@ bool layout(gqa_dtype dtype, int B, int Hq, int Hkv, int C, int d, int t, bool s
     return false;
   if (rows > INT_MAX / 2 || lanes > INT_MAX / 2) return false;
   L.tc = tc_ok && dtype == GQA_BF16 && (d == 64 || d == 128);
-  if (L.tc) {
+  // One scored row is a decode step: its kernel reads the cache at the same
+  // rate and has a tenth of the tile kernel's fixed costs (B = 8, 8001 cells:
+  // 59 us with tiles of 128 rows).
+  L.dec = L.tc && scored && t == 1 && gqa::dechost::splitk_rows_ok(B, Hkv, C);
+  if (L.dec) {
+    gqa::dechost::DecLayout D;
+    if (!gqa::dechost::decode_layout(B, Hq, Hkv, d, &D)) return false;
+    L.ml = D.ml;  // (counters at 0)
+    L.acc = D.acc;
+    L.lse = round256(D.total);
+    L.scores = true;
+  } else if (L.tc) {
     // up to 128 rows fill one row tile; more are taken in pairs of tiles, so
     // that two share each K and V tile
     L.NT = R <= gqa::rows::kM ? 1 : 2;
@@ -77,13 +90,16 @@ bool layout(gqa_dtype dtype, int B, int Hq, int Hkv, int C, int d, int t, bool s
     L.slots = groups * L.ns;
     L.scores = scored;
   }
-  int64_t n;
-  L.groups = round256(gqa::rows::kCounters * sizeof(int));
-  L.ml = L.groups + (L.finish ? round256((size_t)(lanes * L.MG) * sizeof(int2)) : 0);
-  if (!elems(&n, {L.slots, L.group_rows, 8}) || n > INT64_MAX / 8) return false;
-  L.acc = L.ml + round256((size_t)n);
-  if (!elems(&n, {L.slots, L.group_rows, (d + 3) / 4, 16}) || n > INT64_MAX / 8) return false;
-  L.lse = L.acc + round256((size_t)n);
+  if (!L.dec) {
+    int64_t n;
+    // (one more counter than are used here: the decode kernel's region)
+    L.groups = round256((gqa::rows::kCounters + 1) * sizeof(int));
+    L.ml = L.groups + (L.finish ? round256((size_t)(lanes * L.MG) * sizeof(int2)) : 0);
+    if (!elems(&n, {L.slots, L.group_rows, 8}) || n > INT64_MAX / 8) return false;
+    L.acc = L.ml + round256((size_t)n);
+    if (!elems(&n, {L.slots, L.group_rows, (d + 3) / 4, 16}) || n > INT64_MAX / 8) return false;
+    L.lse = L.acc + round256((size_t)n);
+  }
   L.total = L.lse;
   if (scored) {
     if (!elems(&x, {lanes, R, 8}) || x > INT64_MAX / 8) return false;
@@ -156,6 +172,38 @@ gqa_status launch_simt(const Params &p, const DeviceInfo &di, cudaStream_t st) {
   return launched(gqa::launch_dependent(gqa::rows::rows_simt_kernel<T>, dim3((unsigned)grid),
                                         dim3(gqa::rows::kSimtThreads), gqa::rows::simt_smem(p.d),
                                         st, p));
+}
+
+// One row per sequence on the decode kernel, scores and statistics kept.
+gqa_status launch_dec(const Params &p, const Layout &L, const DeviceInfo &di, cudaStream_t st) {
+  const gqa::dechost::DecPlan pl = gqa::dechost::decode_plan(p.Hq, p.Hkv);
+  if (pl.VL > 65535 || p.B > 65535) return GQA_ERR_UNSUPPORTED;
+  gqa::dec::Params x = {};
+  x.q = (const __nv_bfloat16 *)p.q;
+  x.o = (__nv_bfloat16 *)p.o;
+  x.seq_lens = p.seq_lens;
+  x.B = p.B;
+  x.Hq = p.Hq;
+  x.Hkv = p.Hkv;
+  x.C = p.C;
+  x.window = GQA_NO_WINDOW;
+  x.scale_log2 = p.scale_log2;
+  x.r = p.r;
+  x.nsub = pl.nsub;
+  x.VL = pl.VL;
+  x.min_rows = gqa::dechost::kDecodeMinRows;
+  x.counters = p.counters;
+  x.ml = p.ml;
+  x.acc = p.acc;
+  x.status = p.status;
+  x.lens_smem = p.B <= gqa::dec::kLensSmem ? 1 : 0;
+  x.pad = gqa::dechost::kDecodeLanePadBytes / (4 * p.d);  // K and V rows of d bf16
+  x.scores = p.scores;
+  x.lse = p.lse;
+  x.Cp = p.Cp;
+  return p.d == 64
+             ? gqa::dechost::dispatch_splitk_R<64, true>(pl.R, x, p.k, p.v, di.sms, st)
+             : gqa::dechost::dispatch_splitk_R<128, true>(pl.R, x, p.k, p.v, di.sms, st);
 }
 
 struct Operands {
@@ -241,7 +289,9 @@ gqa_status rows_impl(gqa_dtype dtype, const Operands &op, bool tree, int B, int 
   const int64_t grid = tree ? 0 : (int64_t)B * Hkv * cell_blocks;
   if (grid > INT_MAX) return GQA_ERR_UNSUPPORTED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (L.tc) {
+  if (L.dec) {
+    s = launch_dec(p, L, di, st);
+  } else if (L.tc) {
     if (d == 64)
       s = L.NT == 1 ? launch_tc<64, 1>(p, di, st) : launch_tc<64, 2>(p, di, st);
     else
