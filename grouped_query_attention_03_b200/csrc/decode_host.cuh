@@ -87,8 +87,10 @@ inline bool splitk_rows_ok(int B, int Hkv, int C) {
   return (long long)B * Hkv * C < (1LL << 31);
 }
 
+// (static: a program may hold two builds of the library, each with its own
+// kernels and launch state)
 template <int D, int R, bool SC>
-gqa_status launch_splitk(const gqa::dec::Params &p, const void *k_cache,
+static gqa_status launch_splitk(const gqa::dec::Params &p, const void *k_cache,
                          const void *v_cache, int sms, cudaStream_t st) {
   using K = gqa::dec::Cfg<D, R>;
   CUtensorMap mk, mv;
@@ -116,7 +118,7 @@ gqa_status launch_splitk(const gqa::dec::Params &p, const void *k_cache,
 }
 
 template <int D, bool SC = false>
-gqa_status dispatch_splitk_R(int R, const gqa::dec::Params &p, const void *kc,
+static gqa_status dispatch_splitk_R(int R, const gqa::dec::Params &p, const void *kc,
                              const void *vc, int sms, cudaStream_t st) {
   switch (R) {
     case 1: return launch_splitk<D, 1, SC>(p, kc, vc, sms, st);

@@ -122,7 +122,7 @@ constexpr int kLenCache = 128;
 __device__ __forceinline__ Split split_of(const Params &p, int lane, int32_t *cache) {
   long long tot = 0;
   for (int b = lane; b < p.B; b += 32) {
-    const int n = p.seq_lens[b];
+    const int n = __ldcg(p.seq_lens + b);
     if (b < kLenCache) cache[b] = n;
     tot += extent_of(p, n);
   }

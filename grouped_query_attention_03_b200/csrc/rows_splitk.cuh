@@ -154,6 +154,44 @@ struct Walk {
   }
 };
 
+// Where this CTA's range starts.  Warp-wide; the first kLenCache lengths are
+// left in `cache`.
+struct Start {
+  int b, vl, off;
+  long long pos, end, per;
+};
+__device__ __forceinline__ Start start_of(const Params &p, int lane, int32_t *cache) {
+  const Split s = split_of(p, lane, cache);
+  Start r{0, 0, 0, (long long)blockIdx.x * s.per, 0, s.per};
+  r.end = min(s.total, r.pos + s.per);
+  if (r.pos >= r.end) return r;
+  const long long LPB = (long long)p.Hkv * p.MG;
+  long long cum = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int bb = b0 + lane;
+    const long long x =
+        bb < p.B ? extent_of(p, bb < kLenCache ? cache[bb] : __ldcg(p.seq_lens + bb)) * LPB : 0;
+    long long incl = x;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += y;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, cum + incl > r.pos);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      r.b = b0 + src;
+      cum += __shfl_sync(0xffffffffu, incl - x, src);
+      const int ext = (int)(__shfl_sync(0xffffffffu, x, src) / LPB);
+      r.vl = (int)((r.pos - cum) / ext);
+      r.off = (int)((r.pos - cum) - (long long)r.vl * ext);
+      return r;
+    }
+    cum += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return r;
+}
+
 // Clears this thread's value row of an edge tile in shared memory unless it
 // is somebody's (`used`) and finite; true if it was somebody's and was not
 // finite.  Starts at chunk (row & 7) of the swizzled row: no bank conflicts.
@@ -392,43 +430,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   if (warp == 0) {
-    // this CTA's range, and the lane group and tile it starts in
-    const Split s = split_of(p, lane, sh.len);
-    const long long start = (long long)blockIdx.x * s.per, end = min(s.total, start + s.per);
-    const long long LPB = (long long)p.Hkv * p.MG;
-    long long cum = 0;
-    int b = 0, vl = 0, off0 = 0;
-    if (start < end) {
-      for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int bb = b0 + lane;
-        const long long x =
-            bb < p.B ? extent_of(p, bb < kLenCache ? sh.len[bb] : p.seq_lens[bb]) * LPB : 0;
-        long long incl = x;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const long long y = __shfl_up_sync(0xffffffffu, incl, off);
-          if (lane >= off) incl += y;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, cum + incl > start);
-        if (hit) {
-          const int src = __ffs(hit) - 1;
-          b = b0 + src;
-          cum += __shfl_sync(0xffffffffu, incl - x, src);
-          const int ext = (int)(__shfl_sync(0xffffffffu, x, src) / LPB);
-          vl = (int)((start - cum) / ext);
-          off0 = (int)((start - cum) - (long long)vl * ext);
-          break;
-        }
-        cum += __shfl_sync(0xffffffffu, incl, 31);
-      }
-    }
+    const Start at = start_of(p, lane, sh.len);
     if (lane == 0) {
-      sh.b = b;
-      sh.vl = vl;
-      sh.off = off0;
-      sh.start = start;
-      sh.end = end;
-      sh.per = s.per;
+      sh.b = at.b;
+      sh.vl = at.vl;
+      sh.off = at.off;
+      sh.start = at.pos;
+      sh.end = at.end;
+      sh.per = at.per;
     }
   }
   tc::fence_before_sync();
