@@ -192,6 +192,11 @@ __device__ __forceinline__ Start start_of(const Params &p, int lane, int32_t *ca
   return r;
 }
 
+// The bits below position k (k <= 0: none, k >= 32: all).
+__device__ __forceinline__ uint32_t below(int k) {
+  return k >= 32 ? 0xffffffffu : (1u << max(k, 0)) - 1u;
+}
+
 // Clears this thread's value row of an edge tile in shared memory unless it
 // is somebody's (`used`) and finite; true if it was somebody's and was not
 // finite.  Starts at chunk (row & 7) of the swizzled row: no bank conflicts.
@@ -468,6 +473,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     bool first_seg = true;
     int left = 0;                            // the last segment's part was left behind
     int was_b = -1, was_grp = -1;            // whose masks `line`, lo, hi are
+    // the parent of node `row` in this sequence and, ahead of time, the next
+    const int32_t *parents = p.tree ? p.parents : nullptr;
+    int par_b = walk.b, par_next = -2;
+    if (parents && row < p.t && par_b < p.B) par_next = parents[(long long)par_b * p.t + row];
     int lo = 0, hi = 0;                      // cells [lo, hi) this row may read
     Line line;
     line.depth = -1;
@@ -500,8 +509,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (p.parents && sg.b != was_b) {
             // the previous segment's readers are past their masks here
             asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
-            if (row < p.t) sh.par[wg][row] = p.parents[(long long)sg.b * p.t + row];
+            if (row < p.t)
+              sh.par[wg][row] = sg.b == par_b ? par_next : parents[(long long)sg.b * p.t + row];
             asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
+            par_b = sg.b + 1;
+            if (row < p.t && par_b < p.B) par_next = parents[(long long)par_b * p.t + row];
           }
           if (mine) {
             line = line_of(p.parents ? sh.par[wg] : nullptr, i, p.window);
@@ -540,14 +552,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // (NT = 1: by the warps of its own key half)
           const int st = jj % K::STAGES;
           const bool vok = mbar_wait(&sh.v_full[st], (jj / K::STAGES) & 1, &failed);
-          bool used;
-          if (!draft) {
-            used = c0 + row < sg.n;
-          } else {
-            used = row < p.t && (!p.parents || sh.par[wg][row] != -2);
-          }
+          // cells behind the sequence and padding are nobody's; of the others,
+          // finite or not matters only where some row may not read them
+          const bool used = draft ? row < p.t && (!p.parents || sh.par[wg][row] != -2)
+                                  : c0 + row < sg.n;
+          const bool all_read = p.tree && !draft && !(p.window > 0 && c0 < sg.n + p.t - p.window);
           bool odd = false;
-          if (vok) odd = clear_value_row<D>(smem + K::OFF_V + st * K::TILE, row, used);
+          if (vok && !(used && all_read))
+            odd = clear_value_row<D>(smem + K::OFF_V + st * K::TILE, row, used);
           const uint32_t word = __ballot_sync(0xffffffffu, odd);
           if (word) {  // rare: remember which, for add_unfinite
             found = true;
@@ -578,19 +590,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int c = 0; c < NC / 32; ++c) tc::tmem_ld32(tS + c * 32, s + c * 32);
           tc::tmem_wait_ld();
           if (edge) {
-            if (draft) {
+            // the tile's keys that this row reads, as bits
 #pragma unroll
-              for (int w = 0; w < NC / 32; ++w) {
-                const uint32_t bits = NT == 1 ? (wg ? line.bits[2 + w] : line.bits[w]) : line.bits[w];
+            for (int w = 0; w < NC / 32; ++w) {
+              uint32_t bits;
+              if (draft)
+                bits = NT == 1 ? (wg ? line.bits[2 + w] : line.bits[w]) : line.bits[w];
+              else
+                bits = below(hi - c0 - e0 - 32 * w) & ~below(lo - c0 - e0 - 32 * w);
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!((bits >> e) & 1u)) s[w * 32 + e] = masked;
-              }
-            } else {
-              const int a = lo - c0 - e0, z = hi - c0 - e0;
-#pragma unroll
-              for (int e = 0; e < NC; ++e)
-                if (e < a || e >= z) s[e] = masked;
+              for (int e = 0; e < 32; ++e)
+                if (!(bits & (1u << e))) s[w * 32 + e] = masked;
             }
           }
           if (srow) {
