@@ -91,7 +91,8 @@ struct TcShared {
   uint32_t tmem;
   int b, vl, off;          // where this CTA's range starts
   long long start, end;    // its tiles
-  long long per;           // tiles of every CTA
+  long long per;           // positions of every CTA
+  int pad, aligned;        // (see Split)
   int early_last;             // that part was its group's last
   Group late;                 // the last segment's group, to be merged
   int32_t len[kLenCache];
@@ -109,8 +110,8 @@ struct Seg {
 __device__ __forceinline__ Group group_of(const Params &p, const Seg &sg, long long per) {
   Group r;
   r.L = (long long)sg.b * p.Hkv * p.MG + sg.vl;
-  r.c0 = (int)(sg.first / per);
-  r.np = (int)((sg.first + sg.ntiles - 1) / per) - r.c0 + 1;
+  r.c0 = (int)udiv(sg.first, per);
+  r.np = (int)udiv(sg.first + sg.ntiles - 1, per) - r.c0 + 1;
   return r;
 }
 // The first segment, when it ends a lane group that began in an earlier CTA
@@ -122,6 +123,7 @@ __device__ __forceinline__ bool is_early(const Params &p, const Seg &sg, bool fi
 // Walks the CTA's range segment by segment; every role has its own.
 struct Walk {
   int b, vl, off;          // off: into the lane group's extent, pad first
+  int pad, aligned;
   long long pos, end;
   const int32_t *cached;   // the lengths in shared memory
   __device__ __forceinline__ bool next(const Params &p, Seg *s) {
@@ -130,7 +132,7 @@ struct Walk {
       s->n = b < kLenCache ? cached[b] : p.seq_lens[b];
       s->ntiles = tiles_of(p, s->n);
       if (s->ntiles > 0) {
-        const int skip = max(0, p.pad - off);
+        const int skip = max(0, pad - off);
         pos += skip;
         off += skip;
         break;
@@ -141,11 +143,12 @@ struct Walk {
     if (pos >= end) return false;
     s->b = b;
     s->vl = vl;
-    s->j0 = off - p.pad;
+    s->j0 = off - pad;
     s->first = pos - s->j0;
     s->j1 = (int)min((long long)s->ntiles, s->j0 + (end - pos));
     pos += s->j1 - s->j0;
     off = 0;
+    if (aligned) pos = end;  // one group per CTA
     if (++vl == p.Hkv * p.MG) {
       vl = 0;
       ++b;
@@ -158,11 +161,12 @@ struct Walk {
 // left in `cache`.
 struct Start {
   int b, vl, off;
-  long long pos, end, per;
+  long long pos, end;
+  Split split;
 };
 __device__ __forceinline__ Start start_of(const Params &p, int lane, int32_t *cache) {
   const Split s = split_of(p, lane, cache);
-  Start r{0, 0, 0, (long long)blockIdx.x * s.per, 0, s.per};
+  Start r{0, 0, 0, (long long)blockIdx.x * s.per, 0, s};
   r.end = min(s.total, r.pos + s.per);
   if (r.pos >= r.end) return r;
   const long long LPB = (long long)p.Hkv * p.MG;
@@ -170,7 +174,7 @@ __device__ __forceinline__ Start start_of(const Params &p, int lane, int32_t *ca
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int bb = b0 + lane;
     const long long x =
-        bb < p.B ? extent_of(p, bb < kLenCache ? cache[bb] : __ldcg(p.seq_lens + bb)) * LPB : 0;
+        bb < p.B ? extent_of(p, s, bb < kLenCache ? cache[bb] : __ldcg(p.seq_lens + bb)) * LPB : 0;
     long long incl = x;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -182,9 +186,9 @@ __device__ __forceinline__ Start start_of(const Params &p, int lane, int32_t *ca
       const int src = __ffs(hit) - 1;
       r.b = b0 + src;
       cum += __shfl_sync(0xffffffffu, incl - x, src);
-      const int ext = (int)(__shfl_sync(0xffffffffu, x, src) / LPB);
-      r.vl = (int)((r.pos - cum) / ext);
-      r.off = (int)((r.pos - cum) - (long long)r.vl * ext);
+      const long long ext = udiv(__shfl_sync(0xffffffffu, x, src), LPB);
+      r.vl = (int)udiv(r.pos - cum, ext);
+      r.off = (int)((r.pos - cum) - r.vl * ext);
       return r;
     }
     cum += __shfl_sync(0xffffffffu, incl, 31);
@@ -442,7 +446,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       sh.off = at.off;
       sh.start = at.pos;
       sh.end = at.end;
-      sh.per = at.per;
+      sh.per = at.split.per;
+      sh.pad = at.split.pad;
+      sh.aligned = at.split.aligned;
     }
   }
   tc::fence_before_sync();
@@ -450,7 +456,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = sh.tmem;
   bool failed = false;
-  Walk walk{sh.b, sh.vl, sh.off, sh.start, sh.end, sh.len};
+  Walk walk{sh.b, sh.vl, sh.off, sh.pad, sh.aligned, sh.start, sh.end, sh.len};
   Seg sg;
 
   if (warp >= 4) {
@@ -732,7 +738,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const Group gr = group_of(p, sg, sh.per);
       if (p.finish && sg.j0 == 0 && threadIdx.x == 128) p.groups[gr.L] = make_int2(gr.c0, gr.np);
       bool add = false;
-      if (!whole && !is_e && !p.finish && gr.np <= kAddParts) {
+      // (aligned groups' parts end together: looking first would be too early)
+      if (!whole && !is_e && !p.finish && !sh.aligned && gr.np <= kAddParts) {
         bool all = false;
         if (threadIdx.x == 128) all = ld_acquire_gpu(&p.counters[gr.c0]) == gr.np - 1;
         add = any_of_softmax(all, parties);
@@ -852,7 +859,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // now: every tile has been multiplied.  (The first warpgroup takes part in
     // every segment and speaks for both.)
     if (any_of_softmax(ok && left, 256, kBarEnd)) merge_group<D>(p, sh.late, smem, warp - 4);
-    Walk begin{sh.b, sh.vl, sh.off, sh.start, sh.end, sh.len};
+    Walk begin{sh.b, sh.vl, sh.off, sh.pad, sh.aligned, sh.start, sh.end, sh.len};
     if (begin.next(p, &sg) && is_early(p, sg, true, begin.pos < begin.end)) {
       if (!__all_sync(0xffffffffu, mbar_wait(&sh.early_done, 0, &failed))) ok = false;
       if (any_of_softmax(ok && sh.early_last, 256, kBarEnd))
