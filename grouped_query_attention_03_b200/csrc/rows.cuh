@@ -158,7 +158,7 @@ __device__ __forceinline__ Split split_of(const Params &p, int lane, int32_t *ca
   s.total = (tot + (long long)filled * p.pad) * LPB;
   s.per = udiv(s.total + p.ctas - 1, p.ctas);
   if (s.per < p.min_tiles) s.per = p.min_tiles;
-  if (p.B <= 32 && filled * LPB <= p.ctas && s.total < (1 << 24)) {
+  if (p.B <= 32 && s.per > 1 && filled * LPB <= p.ctas && s.total < (1 << 24)) {
     // the smallest share with which whole CTAs suffice, if it is near
     const int most = (int)(s.per + s.per / 4);
     int per = max((int)udiv(tot * LPB + p.ctas - 1, p.ctas), p.min_tiles), used = 0;
