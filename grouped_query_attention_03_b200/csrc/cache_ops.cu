@@ -9,6 +9,7 @@
 namespace {
 
 using namespace gqa::host;
+using gqa::evict::kMaxCluster;
 
 // Vectors a row is moved in: 16 bytes where rows and buffers allow, else
 // elements.
@@ -189,7 +190,10 @@ gqa_status gqa_cache_evict(gqa_dtype dtype, const void *k_cache, const void *v_c
       (in_place && C != C_out))
     return GQA_ERR_SHAPE;
   if (C > (1 << 30) || C_out > (1 << 30)) return GQA_ERR_UNSUPPORTED;
-  if ((int64_t)B * Hkv > INT_MAX) return GQA_ERR_UNSUPPORTED;
+  // grids (a lane's cluster, its column slices), before anything is enqueued
+  int64_t blocks;
+  if (!elems(&blocks, {B, Hkv, std::max(kMaxCluster, 2 * (d / 4 + 1))}) || blocks > INT_MAX)
+    return GQA_ERR_UNSUPPORTED;
   DeviceInfo di;
   gqa_status s = device_info(&di);
   if (s != GQA_OK) return s;

@@ -381,8 +381,8 @@ gqa_status gqa_qk_norm_rope(gqa_dtype dtype, const void *qkv, int64_t batch_stri
  *            with gqa_decode's rules: zero-filled once before its first use,
  *            left ready for the next call of any shape by every call that
  *            completes, zeroed again after GQA_ERR_TIMEOUT; calls sharing it
- *            must be ordered.  gqa_decode_tree and gqa_decode_scored may
- *            share one, not with gqa_decode
+ *            must be ordered (calls of gqa_decode and its relatives, of
+ *            gqa_decode_tree and of gqa_decode_scored may share one)
  *   dev_status device int32 (required)
  * A length outside [0, C] sets GQA_ERR_CAPACITY and zeroes that sequence's
  * output.  A parent outside [-2, i), or one that is padding or itself

@@ -212,11 +212,52 @@ def test_evict_refuses_a_bad_length_and_leaves_that_sequence(cuda_lib):
         assert torch.equal(outs[0][1, 0, :32].cpu(), kc[1, 0, stay])
 
 
+def test_evict_and_scored_replay_from_a_graph(cuda_lib):
+    """A captured step (scored rows, then eviction in place) replays on what is
+    in its buffers then, and leaves rows behind the last sequence alone."""
+    B, Hq, Hkv, C, d = 2, 8, 2, 1200, 128
+    lens = [1200, 700]
+    q, kc, vc, _, _ = make(B, Hq, Hkv, C, d, 1, lens, 21)
+    kc, vc = torch.nan_to_num(kc), torch.nan_to_num(vc, posinf=1.0)
+    dev = [x.to(DEV) for x in (q[:, :, 0].contiguous(), kc, vc)]
+    lt = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    w, st = torch.zeros(B, Hkv, C, device=DEV), cuda_lib.new_status(DEV)
+    ws = cuda_lib.decode_scored_workspace(dev[0], dev[1])
+    kept = torch.empty(B, Hkv, 800, dtype=torch.int32, device=DEV)
+    o = torch.empty_like(dev[0])
+
+    def step():
+        cuda_lib.decode_scored(*dev, w, lt, out=o, workspace=ws, status=st)
+        cuda_lib.cache_evict(dev[1], dev[2], w, lt, 800, 64, kept=kept, status=st)
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for seed in (1, 2):
+        dev[0].copy_(synthetic.normal(dev[0].shape, seed, 1.0, BF))
+        dev[1].copy_(kc), dev[2].copy_(vc), w.zero_(), lt.copy_(torch.tensor(lens))
+        g.replay()
+        torch.cuda.synchronize()
+        want, mag, wv, _ = so.scored(f64(dev[0])[:, :, None], f64(kc), f64(vc), lens)
+        assert_mix(o[:, :, None], want, mag, BF)
+        assert int(st.item()) == 0 and lt.tolist() == [800, 700]
+        for h in range(Hkv):
+            rows = kept[0, h].long().cpu()
+            assert torch.equal(dev[1][0, h, :800].cpu(), kc[0, h, rows])
+            # the survivors are the heaviest up to the weights' rounding
+            lost = np.setdiff1d(np.arange(1200 - 64), rows.numpy())
+            stay = rows.numpy()[rows.numpy() < 1200 - 64]
+            assert wv[0, h, stay].min() >= wv[0, h, lost].max() * (1 - 1e-4)
+            assert kept[1, h, :700].tolist() == list(range(700)) and torch.all(kept[1, h, 700:] == -1)
+            assert torch.equal(dev[1][1, h].cpu(), kc[1, h]) and torch.equal(dev[2][0, h, 800:].cpu(), vc[0, h, 800:])
+
+
 # ------------------------------------------------------------------- commit
 @pytest.mark.parametrize("apart", [False, True])
 @pytest.mark.parametrize("dtype,B,Hkv,C,d,t,P", [
     (BF, 3, 2, 40, 128, 20, 6), (BF, 1, 1, 9, 64, 1, 1), (BF, 2, 2, 40, 33, 12, 12),
-    (F32, 3, 2, 40, 64, 20, 9), (BF, 70, 8, 30, 128, 30, 20)])
+    (F32, 3, 2, 40, 64, 20, 9), (BF, 70, 8, 30, 128, 30, 20),
+    (BF, 5, 4, 30, 128, 9, 4), (BF, 7, 6, 30, 128, 9, 4)])  # clusters of 3 and of 6 CTAs
 def test_commit(cuda_lib, dtype, B, Hkv, C, d, t, P, apart):
     g = torch.Generator()
     g.manual_seed(B + P)

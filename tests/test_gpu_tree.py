@@ -283,3 +283,73 @@ def test_a_long_cache_splits_over_all_sms(cuda_lib):
     o, st = run(cuda_lib, ins, par, lens)
     assert st == 0
     assert_mix(o, want, mag, BF)
+
+
+RUNNING = [
+    # B, Hq, Hkv, C, d, t, window, padding: more than 32 sequences, so that a
+    # CTA's range runs from one lane group into the next
+    (40, 8, 2, 3000, 128, 20, None, 3),
+    (40, 8, 1, 1500, 128, 40, None, 9),    # 320 rows: pairs of row tiles, two groups
+    (33, 4, 2, 2000, 64, 70, 700, 5),      # 140 rows: a second tile of 12, window
+    (150, 2, 1, 900, 128, 5, None, 0),     # more lengths than the kernel keeps at hand
+]
+
+
+@pytest.mark.parametrize("case", RUNNING, ids=lambda c: f"B{c[0]}Hq{c[1]}Hkv{c[2]}d{c[4]}t{c[5]}w{c[6]}")
+def test_ranges_that_cross_lane_groups(cuda_lib, case):
+    """Early, whole, middle and last parts; refused sequences in between."""
+    B, Hq, Hkv, C, d, t, window, pad = case
+    lens = [(b * 733) % (C + 1) for b in range(B)]
+    lens[1], lens[B // 2], lens[3] = -5, C + 1, C
+    ins = make(B, Hq, Hkv, C, d, t, lens, t)
+    par = random_tree(B, t, t, pad)
+    want, mag = so.tree(*[f64(x) for x in ins], par.numpy(), lens, window=window)
+    o, st = run(cuda_lib, ins, par, lens, window=window)
+    assert st == 5
+    assert_mix(o, want, mag, BF)
+    again, _ = run(cuda_lib, ins, par, lens, window=window)
+    assert torch.equal(o, again)
+
+
+def test_an_empty_cache(cuda_lib):
+    """Capacity 0: the drafts alone."""
+    for d, dtype in ((128, BF), (64, F32)):
+        ins = make(2, 4, 2, 0, d, 6, [0, 0], 3, dtype)
+        par = random_tree(2, 6, 4)
+        want, mag = so.tree(*[f64(x) for x in ins], par.numpy(), [0, 0])
+        o, st = run(cuda_lib, ins, par, [0, 0])
+        assert st == 0
+        assert_mix(o, want, mag, dtype)
+
+
+def test_one_workspace_with_the_other_decodes(cuda_lib):
+    """decode, decode_tree and decode_scored take turns on one workspace, and
+    two calls run at once on two streams with a workspace each."""
+    B, Hq, Hkv, C, d, t = 2, 8, 2, 2500, 128, 12
+    lens = [2500, 1300]
+    ins = make(B, Hq, Hkv, C, d, t, lens, 3)
+    par = random_tree(B, t, 4)
+    q, kc, vc, kd, vd = [x.to(DEV) for x in ins]
+    lt, pd = torch.tensor(lens, dtype=torch.int32, device=DEV), par.to(DEV)
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device=DEV)
+    q1 = q[:, :, 0].contiguous()
+    alone = (cuda_lib.decode_tree(q, kc, vc, kd, vd, pd, lt), cuda_lib.decode(q1, kc, vc, lt),
+             cuda_lib.decode_scored(q1, kc, vc, torch.zeros(B, Hkv, C, device=DEV), lt),
+             cuda_lib.decode_scored(q, kc, vc, torch.zeros(B, Hkv, C, device=DEV), lt))
+    for _ in range(3):
+        w1, w2 = torch.zeros(B, Hkv, C, device=DEV), torch.zeros(B, Hkv, C, device=DEV)
+        got = (cuda_lib.decode_tree(q, kc, vc, kd, vd, pd, lt, workspace=ws),
+               cuda_lib.decode(q1, kc, vc, lt, workspace=ws),
+               cuda_lib.decode_scored(q1, kc, vc, w1, lt, workspace=ws),
+               cuda_lib.decode_scored(q, kc, vc, w2, lt, workspace=ws))
+        for a, b in zip(alone, got):
+            assert torch.equal(a, b)
+    side = [torch.cuda.Stream() for _ in range(2)]
+    wss = [cuda_lib.decode_tree_workspace(q, kc) for _ in range(2)]
+    outs = [torch.empty_like(q) for _ in range(2)]
+    torch.cuda.synchronize()
+    for rep in range(10):
+        for s, w, o in zip(side, wss, outs):
+            cuda_lib.decode_tree(q, kc, vc, kd, vd, pd, lt, out=o, workspace=w, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], alone[0]) and torch.equal(outs[1], alone[0])
