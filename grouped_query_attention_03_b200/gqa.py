@@ -130,7 +130,7 @@ def _run(dev, what, fn, *args):
     """Call a C entry point with `dev` (the tensors' device) current: the
     library looks up per-device state (SM count, fixed scratch address) on
     the current device."""
-    if dev.index == torch.cuda.current_device():
+    if dev.index == _current_device():
         status = fn(*args)
     else:
         with torch.cuda.device(dev):
@@ -171,8 +171,10 @@ def _ptr(t, name, dtype=None, device=None):
 
 
 # The current stream's handle without building a torch.cuda.Stream around it
-# (2 us of a small call), where this torch has it.
+# (2 us of a small call), and the current device without the check that CUDA
+# has been initialised (a tensor on it exists), where this torch has them.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream, device):
@@ -184,7 +186,7 @@ def _stream(stream, device):
 
 
 def _check_lens(lens, B):
-    if lens.dim() != 1 or lens.shape[0] != B:
+    if lens.shape != (B,):
         raise ValueError(f"lengths must be [{B}]")
 
 
@@ -434,7 +436,7 @@ def qk_norm_rope(qkv, Hq, Hkv, d, *, q_weight=None, k_weight=None, eps=1e-6, inv
     (i, i + rot/2) or (interleaved) (2i, 2i + 1); positions int32 [B,T] or
     [A,B,T] (None: 0..T-1), axes: the axis of each pair (a list of rot/2
     numbers below A; None: all 0)."""
-    if qkv.dim() != 3 or (qkv.shape[2] > 1 and qkv.stride(2) != 1):
+    if qkv.dim() != 3 or (qkv.stride(2) != 1 and qkv.shape[2] > 1):
         raise ValueError("qkv must be [B,T,width] with contiguous rows")
     B, T, width = qkv.shape
     if width < (Hq + 2 * Hkv) * d:
@@ -444,9 +446,10 @@ def qk_norm_rope(qkv, Hq, Hkv, d, *, q_weight=None, k_weight=None, eps=1e-6, inv
     if positions is None:
         naxes = 1
     else:
-        if tuple(positions.shape[-2:]) != (B, T) or positions.dim() not in (2, 3):
+        at = positions.shape
+        naxes = at[0] if len(at) == 3 else 1
+        if at != (B, T) and at != (naxes, B, T):
             raise ValueError("positions must be [B,T] or [axes,B,T]")
-        naxes = positions.shape[0] if positions.dim() == 3 else 1
     pair_axis = None
     if axes is not None:
         if len(axes) != half:
@@ -459,7 +462,8 @@ def qk_norm_rope(qkv, Hq, Hkv, d, *, q_weight=None, k_weight=None, eps=1e-6, inv
     if out is None:
         out = tuple(torch.empty((B, h, T, d), dtype=dt, device=dev) for h in (Hq, Hkv, Hkv))
     q, k, v = out
-    if q.shape != (B, Hq, T, d) or k.shape != (B, Hkv, T, d) or v.shape != k.shape:
+    rows = (B, Hkv, T, d)
+    if q.shape != (B, Hq, T, d) or k.shape != rows or v.shape != rows:
         raise ValueError("out must be q [B,Hq,T,d], k and v [B,Hkv,T,d]")
     if not qkv.is_cuda:
         raise ValueError("qkv must live in CUDA device memory")
@@ -493,11 +497,12 @@ def decode_tree(q, k_cache, v_cache, k_draft, v_draft, parents, seq_lens, *, win
     k_draft/v_draft [B,Hkv,t,d] the nodes' rows (not in the cache yet).  Node
     i reads the committed cells and its own line in the tree; parents [B,t]
     int32: -1 a root, -2 padding, None a chain."""
-    B, Hq, t, d = q.shape
-    Hkv, C = k_cache.shape[1], k_cache.shape[2]
-    if k_cache.shape != (B, Hkv, C, d) or v_cache.shape != k_cache.shape:
+    B, Hq, t, d = shape = q.shape
+    cells, drafts = k_cache.shape, k_draft.shape
+    Hkv, C = cells[1], cells[2]
+    if cells != (B, Hkv, C, d) or v_cache.shape != cells:
         raise ValueError("cache shape mismatch")
-    if k_draft.shape != (B, Hkv, t, d) or v_draft.shape != k_draft.shape:
+    if drafts != (B, Hkv, t, d) or v_draft.shape != drafts:
         raise ValueError("drafted K/V must be [B,Hkv,t,d]")
     if parents is not None and parents.shape != (B, t):
         raise ValueError("parents must be [B, t]")
@@ -506,7 +511,7 @@ def decode_tree(q, k_cache, v_cache, k_draft, v_draft, parents, seq_lens, *, win
         scale = d ** -0.5
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    elif out.shape != q.shape:
+    elif out.shape != shape:
         raise ValueError("out must have the shape of q")
     dev, dt = q.device, q.dtype
     if workspace is None:
@@ -529,18 +534,20 @@ def tree_commit(k_cache, v_cache, k_draft, v_draft, path, path_lens, seq_lens, *
     [B,P], ascending nodes) of k_draft/v_draft [B,Hkv,t,d] go to cells
     seq_lens[b] on, and lens_out (default: seq_lens itself) becomes seq_lens
     + path_lens (all-or-nothing on the device).  Returns the status word."""
-    B, Hkv, C, d = k_cache.shape
-    t = k_draft.shape[2]
-    if v_cache.shape != k_cache.shape:
+    B, Hkv, C, d = cells = k_cache.shape
+    drafts, steps = k_draft.shape, path.shape
+    t = drafts[2]
+    if v_cache.shape != cells:
         raise ValueError("cache shape mismatch")
-    if k_draft.shape != (B, Hkv, t, d) or v_draft.shape != k_draft.shape:
+    if drafts != (B, Hkv, t, d) or v_draft.shape != drafts:
         raise ValueError("drafted K/V must be [B,Hkv,t,d]")
-    if path.dim() != 2 or path.shape[0] != B or path_lens.shape != (B,):
+    if len(steps) != 2 or steps[0] != B or path_lens.shape != (B,):
         raise ValueError("path must be [B,P] and path_lens [B]")
     _check_lens(seq_lens, B)
     if lens_out is None:
         lens_out = seq_lens
-    _check_lens(lens_out, B)
+    else:
+        _check_lens(lens_out, B)
     dev, dt = k_cache.device, k_cache.dtype
     st = new_status(dev) if status is None else status
     _run(dev, "gqa_tree_commit", lib().gqa_tree_commit,
@@ -548,7 +555,7 @@ def tree_commit(k_cache, v_cache, k_draft, v_draft, path, path_lens, seq_lens, *
          _ptr(k_draft, "k_draft", dt, dev), _ptr(v_draft, "v_draft", dt, dev),
          _ptr(path, "path", torch.int32, dev), _ptr(path_lens, "path_lens", torch.int32, dev),
          _ptr(seq_lens, "seq_lens", torch.int32, dev), _ptr(lens_out, "lens_out", torch.int32, dev),
-         B, Hkv, C, d, t, path.shape[1], _ptr(st, "status", torch.int32, dev), _stream(stream, dev))
+         B, Hkv, C, d, t, steps[1], _ptr(st, "status", torch.int32, dev), _stream(stream, dev))
     return st
 
 
@@ -566,10 +573,11 @@ def decode_scored(q, k_cache, v_cache, weights, seq_lens, *, scale=None, out=Non
                   status=None, stream=None):
     """decode() (q [B,Hq,d]) or decode_multi() (q [B,Hq,t,d]) that also adds
     to weights [B,Hkv,C] float32 the softmax weights each cell received."""
-    t = q.shape[2] if q.dim() == 4 else 1
-    B, Hq, d = q.shape[0], q.shape[1], q.shape[-1]
-    Hkv, C = k_cache.shape[1], k_cache.shape[2]
-    if k_cache.shape != (B, Hkv, C, d) or v_cache.shape != k_cache.shape:
+    shape, cells = q.shape, k_cache.shape
+    B, Hq, d = shape[0], shape[1], shape[-1]
+    t = shape[2] if len(shape) == 4 else 1
+    Hkv, C = cells[1], cells[2]
+    if cells != (B, Hkv, C, d) or v_cache.shape != cells:
         raise ValueError("cache shape mismatch")
     if weights.shape != (B, Hkv, C):
         raise ValueError("weights must be [B,Hkv,C]")
@@ -578,7 +586,7 @@ def decode_scored(q, k_cache, v_cache, weights, seq_lens, *, scale=None, out=Non
         scale = d ** -0.5
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    elif out.shape != q.shape:
+    elif out.shape != shape:
         raise ValueError("out must have the shape of q")
     dev, dt = q.device, q.dtype
     if workspace is None:
@@ -601,21 +609,25 @@ def cache_evict(k_cache, v_cache, weights, seq_lens, budget, recent, *, k_out=No
     weights_out [B,Hkv,C_out].  lens_out (default: seq_lens itself) becomes
     min(seq_lens, budget).  Returns kept [B,Hkv,budget] int32, the cell that
     each kept row came from (-1 behind them)."""
-    B, Hkv, C, d = k_cache.shape
-    if v_cache.shape != k_cache.shape or weights.shape != (B, Hkv, C):
+    B, Hkv, C, d = cells = k_cache.shape
+    if v_cache.shape != cells or weights.shape != (B, Hkv, C):
         raise ValueError("cache and weights shape mismatch")
+    C_out = C
     if k_out is None and v_out is None and weights_out is None:
         k_out, v_out, weights_out = k_cache, v_cache, weights
     elif k_out is None or v_out is None or weights_out is None:
         raise ValueError("k_out, v_out and weights_out come together")
-    C_out = k_out.shape[2]
-    if k_out.shape != (B, Hkv, C_out, d) or v_out.shape != k_out.shape or \
-            weights_out.shape != (B, Hkv, C_out):
-        raise ValueError("output shape mismatch")
+    else:
+        new_cells = k_out.shape
+        C_out = new_cells[2]
+        if new_cells != (B, Hkv, C_out, d) or v_out.shape != new_cells or \
+                weights_out.shape != (B, Hkv, C_out):
+            raise ValueError("output shape mismatch")
     _check_lens(seq_lens, B)
     if lens_out is None:
         lens_out = seq_lens
-    _check_lens(lens_out, B)
+    else:
+        _check_lens(lens_out, B)
     dev, dt = k_cache.device, k_cache.dtype
     if kept is None:
         kept = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=dev)
