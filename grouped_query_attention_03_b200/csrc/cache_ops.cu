@@ -25,10 +25,11 @@ RowVec row_vec(gqa_dtype dtype, int d, std::initializer_list<const void *> ptrs)
   return ok ? RowVec{16, d * esz / 16} : RowVec{esz, d};
 }
 
-// Columns a tree commit may move with one cluster of 8 CTAs and still hide
-// behind its latency; larger in-place commits take the whole GPU and a
-// second launch for the lengths.
-constexpr int64_t kClusterCols = 32768;
+// Columns a tree commit moves with one cluster of 8 CTAs; larger in-place
+// commits take the whole GPU and a second launch for the lengths (2048
+// columns, 8 lanes of 8 sequences: 5.3 us against 6.6; 4096: 6.6 both; 8192:
+// 9.1 against 7.5).
+constexpr int64_t kClusterCols = 4096;
 
 template <typename V>
 gqa_status launch_commit(void *kc, void *vc, const void *kd, const void *vd,
@@ -78,16 +79,23 @@ gqa_status launch_select_k(const gqa::evict::Params &p, int cluster, cudaStream_
   return launched(cudaLaunchKernelEx(&cfg, gqa::evict::evict_select_kernel<KPT>, p, cluster));
 }
 
-// CTAs per lane: as many as the lanes leave SMs for, up to 8, and as many as
-// its capacity needs to be held in registers (32 keys a thread); a lane that
-// 8 CTAs cannot hold is read again for every digit by one.
+// CTAs per lane.  A cluster's launch, barriers and remote counts cost more
+// than reading a few thousand cells does (8 lanes of 4000 cells, to 2048:
+// 10.2 us with a CTA each, 11.4 with two, 13.8 with four, 18.2 with eight), so
+// a CTA gets at least 8 strips of 512 cells, and a cluster up to 4 of them
+// while the lanes leave SMs for more (8 lanes of 32768 cells, to 4096: 42 us
+// with one, 20.8 with two, 17.9 with four, 25.5 with eight; 64 lanes of 8000,
+// to 4096: 57.4, 56.4, 58.1).  Longer lanes take as many CTAs, up to 8, as
+// hold their keys in registers (32 a thread); a lane that 8 cannot hold is
+// read again for every digit by one.
 gqa_status launch_select(const gqa::evict::Params &p, int sms, cudaStream_t st) {
   using namespace gqa::evict;
   const int64_t lanes = (int64_t)p.B * p.Hkv;
   const int64_t strips = ((int64_t)p.C + kSelThreads - 1) / kSelThreads;
   int cluster = 1;
-  while (cluster < kMaxCluster && strips > cluster &&
-         (lanes * cluster * 2 <= 2 * sms || strips > 32 * cluster))
+  while (cluster < kMaxCluster &&
+         ((cluster < 4 && strips > 8 * cluster && lanes * cluster * 2 <= sms) ||
+          strips > 32 * cluster))
     cluster *= 2;
   const int64_t kpt = (strips + cluster - 1) / cluster;
   if (lanes * cluster > INT_MAX) return GQA_ERR_UNSUPPORTED;
@@ -132,9 +140,10 @@ gqa_status gqa_tree_commit(gqa_dtype dtype, void *k_cache, void *v_cache, const 
   if (dtype != GQA_F32 && dtype != GQA_BF16) return GQA_ERR_UNSUPPORTED;
   if (B < 0 || C < 0 || t_new < 0 || max_path < 0) return GQA_ERR_SHAPE;
   if (Hkv <= 0 || d <= 0) return GQA_ERR_SHAPE;
-  int64_t nc, nd, np;
+  int64_t nc, nd, np, cols;
   if (!elems(&nc, {B, Hkv, C, d}) || !elems(&nd, {B, Hkv, t_new, d}) ||
-      !elems(&np, {B, max_path}) || nc > INT64_MAX / 8 || nd > INT64_MAX / 8)
+      !elems(&np, {B, max_path}) || !elems(&cols, {B, Hkv, d, 8}) || nc > INT64_MAX / 8 ||
+      nd > INT64_MAX / 8 || d > INT_MAX / 8)
     return GQA_ERR_OVERFLOW;
   if (B == 0) return GQA_OK;
   if (!path_lens || !seq_lens || !lens_out || !dev_status) return GQA_ERR_NULL;
@@ -175,7 +184,7 @@ gqa_status gqa_cache_evict(gqa_dtype dtype, const void *k_cache, const void *v_c
   if (recent > budget || budget > C_out) return GQA_ERR_CAPACITY;
   int64_t nc, no;
   if (!elems(&nc, {B, Hkv, C, d}) || !elems(&no, {B, Hkv, C_out, d}) || nc > INT64_MAX / 8 ||
-      no > INT64_MAX / 8)
+      no > INT64_MAX / 8 || d > INT_MAX / 8)
     return GQA_ERR_OVERFLOW;
   if (B == 0) return GQA_OK;
   // nothing to read, or nothing to keep and no weights to clear: the lengths

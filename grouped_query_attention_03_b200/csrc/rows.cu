@@ -19,22 +19,19 @@ using gqa::rows::Params;
 constexpr int kMaxCtas = 256;
 constexpr int kSimtCtas = 592;
 
-// Tiles a CTA takes at least, and what a lane group costs it in tiles.
-#ifndef GQA_ROWS_MIN_TILES
-#define GQA_ROWS_MIN_TILES 1
-#endif
-#ifndef GQA_ROWS_PAD
-#define GQA_ROWS_PAD 3
-#endif
-constexpr int kMinTiles = GQA_ROWS_MIN_TILES;
-constexpr int kPadTiles = GQA_ROWS_PAD;
+// What a lane group costs a CTA besides its tiles, in tiles (64 ragged
+// sequences, 63 nodes: 120 us with 2, 111 with 3 and with 4, 114 with 5).
+constexpr int kPadTiles = 3;
 
 // Rows times parts that the last CTA to count a lane group's parts merges
-// itself; more than that is shared by all SMs in a kernel of its own.
-#ifndef GQA_ROWS_MERGE
-#define GQA_ROWS_MERGE 800
-#endif
-constexpr int kMergeRows = GQA_ROWS_MERGE;
+// itself; more than that is shared by all SMs in a kernel of its own (d = 128,
+// r = 4: 8 sequences of 8000 cells, 26 nodes, 4 parts: 56 us, 63 with the
+// kernel; 2 sequences, 8 nodes, 10 parts: 25.1 us with it, 27.9 without; one of
+// 1000 cells: 13.3 and 19.5).
+constexpr int kMergeRows = 800;
+
+// Calls that share a workspace find each other's counters at the same place.
+static_assert(gqa::rows::kCounters == gqa::dec::kCtrFinish, "the counters' region");
 
 struct Layout {
   bool tc = false;
@@ -78,6 +75,8 @@ bool layout(gqa_dtype dtype, int B, int Hq, int Hkv, int C, int d, int t, bool s
     // what the last CTA to count them would have to read.
     const int64_t parts = kMaxCtas / 2 / std::max<int64_t>(lanes * L.MG, 1) + 2;
     L.finish = parts > gqa::rows::kAddParts || parts * L.group_rows > kMergeRows;
+    // (8 lanes of 32768 cells, d = 128: 32 rows 53.8 us with the scores kept, 59.0
+    // with the keys read again; 64 rows 74.6 and 60.5)
     L.scores = scored && R <= d / 4;
   } else {
     L.group_rows = gqa::rows::kSR;
@@ -275,7 +274,6 @@ gqa_status rows_impl(gqa_dtype dtype, const Operands &op, bool tree, int B, int 
   p.group_rows = L.group_rows;
   p.MG = L.MG;
   p.ctas = std::min(kMaxCtas, di.sms);
-  p.min_tiles = kMinTiles;
   p.pad = kPadTiles;
   p.ns = L.ns;
   p.scale_log2 = scale * gqa::kLog2e;

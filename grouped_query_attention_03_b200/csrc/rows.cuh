@@ -49,7 +49,7 @@ struct Params {
   int Cp;                   // row pitch of scores: C rounded up to whole tiles
   int group_rows;           // rows one CTA works on (a slot's rows)
   int MG;                   // groups of group_rows rows per lane
-  int ctas, min_tiles, pad; // tensor-core split (ctas CTAs share all tiles)
+  int ctas, pad;            // tensor-core split (ctas CTAs share all tiles)
   int ns;                   // CUDA-core split (ns parts per lane), else 0
   int finish;               // rows_finish_kernel merges
   float scale_log2;
@@ -157,17 +157,17 @@ __device__ __forceinline__ Split split_of(const Params &p, int lane, int32_t *ca
   s.aligned = 0;
   s.total = (tot + (long long)filled * p.pad) * LPB;
   s.per = udiv(s.total + p.ctas - 1, p.ctas);
-  if (s.per < p.min_tiles) s.per = p.min_tiles;
+  if (s.per < 1) s.per = 1;
   if (p.B <= 32 && s.per > 1 && filled * LPB <= p.ctas && s.total < (1 << 24)) {
     // the smallest share with which whole CTAs suffice, if it is near
     const int most = (int)(s.per + s.per / 4);
-    int per = max((int)udiv(tot * LPB + p.ctas - 1, p.ctas), p.min_tiles), used = 0;
+    int per = max((int)udiv(tot * LPB + p.ctas - 1, p.ctas), 1), used = 0;
     for (int i = 0; i < 8 && per <= most; ++i) {
       used = (int)LPB * (int)__reduce_add_sync(0xffffffffu, (unsigned)((nt + per - 1) / per));
       if (used <= p.ctas) {
         // as small as gives every group the same number of parts
         const int np = max(1, (nt + per - 1) / per);
-        per = max((int)__reduce_max_sync(0xffffffffu, (unsigned)((nt + np - 1) / np)), p.min_tiles);
+        per = max((int)__reduce_max_sync(0xffffffffu, (unsigned)((nt + np - 1) / np)), 1);
         s.aligned = 1;
         s.pad = 0;
         s.per = per;

@@ -1,6 +1,6 @@
-// rows_splitk.cuh -- tcgen05/TMEM split-K attention of up to 128 query rows
-// per head over a cache: gqa_decode_tree and gqa_decode_scored for bf16 with
-// d = 64 or 128 (sm_100a).  Which keys a row reads, the split over CTAs and
+// rows_splitk.cuh -- tcgen05/TMEM split-K attention of a KV group's query rows
+// over a cache: gqa_decode_tree and gqa_decode_scored for bf16 with d = 64 or
+// 128 (sm_100a).  Which keys a row reads, the split over CTAs and
 // the merge are in rows.cuh.
 //
 // The rows of a KV group (r heads x t_new rows, consecutive in q) fill the
@@ -24,9 +24,13 @@
 // tile j, and two O; NT = 2 has one S and one O per row tile, and the two
 // take turns.
 //
-// Bound by HBM while a group has at most about 256 rows: a 128-key tile is
-// 4 d * 128 bytes, 1.5 us of an SM's share of the bandwidth at d = 128,
-// against 0.4 us of MMA and about 0.8 us of softmax per row tile.
+// Bound by HBM with one row tile: a 128-key tile is 4 d * 128 bytes, 1.5 us of
+// an SM's share of the bandwidth at d = 128 (8 sequences of 8000 cells, 26
+// nodes, 32 heads on 8: 56 us, 4.7 TB/s, of which 11 us start and end).  Two
+// row tiles take 2.35 us per 128 keys (1.06 PFLOP/s), each tile's products and
+// softmax in turn with the other's; short segments then show what a segment
+// costs besides its tiles, 7 to 9 us of masks, queries and O's way out (64
+// ragged sequences, 63 nodes, 8 heads on 1: 111 us, 0.6 PFLOP/s).
 //
 // What a row may not read never reaches it: its scores are masked by a
 // select, and since 0 * NaN is not 0, value rows of an edge tile that some

@@ -433,8 +433,8 @@ gqa_status gqa_tree_commit(gqa_dtype dtype, void *k_cache, void *v_cache, const 
  *   weights  device float [B,Hkv,C], in/out; cells >= n_b are left alone
  *   seq_lens device int32 [B], n_b in [t_new, C]
  *   workspace  gqa_decode_scored_workspace_bytes(...) bytes, 256-byte
- *            aligned, with the rules of gqa_decode_tree's (it holds the
- *            scores: 4 bytes per query row and cell)
+ *            aligned, with the rules of gqa_decode_tree's (with few rows
+ *            it holds the scores: 4 bytes per query row and cell)
  * A length outside [t_new, C] sets GQA_ERR_CAPACITY, zeroes that sequence's
  * output and leaves its weights.  t_new > GQA_MAX_TREE returns
  * GQA_ERR_UNSUPPORTED.

@@ -33,6 +33,15 @@ SCORED = [
     (F32, 2, 4, 2, 128, 64, 1, [128, 33]),
     (F32, 1, 6, 2, 300, 128, 17, [290]),
     (F32, 1, 2, 1, 100, 256, 100, [100]),
+    # one row: groups of 3, 10, 20 and 32 heads, more sequences than the
+    # kernels keep lengths of
+    (BF, 2, 6, 2, 300, 64, 1, [300, 7]),
+    (BF, 2, 20, 2, 1500, 128, 1, [1500, 777]),
+    (BF, 1, 40, 2, 2100, 64, 1, [2099]),
+    (BF, 2, 64, 2, 700, 128, 1, [650, 700]),
+    (BF, 4500, 1, 1, 20, 64, 1, [1 + b % 20 for b in range(4500)]),
+    (BF, 140, 2, 1, 300, 64, 3, [3 + (b * 37) % 298 for b in range(140)]),
+    (BF, 140, 32, 1, 200, 128, 4, [4 + (b * 37) % 197 for b in range(140)]),
 ]
 
 
@@ -141,8 +150,12 @@ EVICT = [
     (BF, 2, 2, 1500, 64, [1500, 1025], 512, 0, "ties"),
     (BF, 1, 3, 1024, 128, [1023], 1000, 3, "equal"),
     (BF, 2, 3, 2100, 64, [2100, 2000], 777, 50, "wild"),
-    (BF, 1, 2, 9000, 64, [8900], 4096, 512, "tail"),       # 32 keys a thread
-    (BF, 1, 1, 40000, 64, [39999], 5000, 100, "wild"),     # longer than the registers
+    (BF, 1, 2, 9000, 64, [8900], 4096, 512, "tail"),
+    (BF, 1, 1, 40000, 64, [39999], 5000, 100, "wild"),     # 32 keys a thread, 4 CTAs
+    (BF, 1, 1, 70000, 8, [69999], 30000, 0, "wild"),       # 8 CTAs
+    (BF, 1, 1, 140000, 8, [139999], 5000, 100, "wild"),    # longer than the registers
+    (BF, 1, 1, 140000, 8, [139999], 139998, 0, "ties"),
+    (BF, 40, 4, 9000, 8, [(b * 997) % 9001 for b in range(40)], 4096, 512, "ties"),  # a CTA per lane
     (BF, 1, 1, 40000, 64, [33000], 32999, 0, "ties"),
     (BF, 1, 2, 100, 33, [100], 37, 5, "ties"),             # odd rows
     (F32, 2, 2, 200, 64, [200, 150], 64, 16, "wild"),

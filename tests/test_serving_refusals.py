@@ -114,6 +114,7 @@ def test_commit_refusals(gqa):
     for name in ("kc", "vc", "kd", "vd", "path", "pl", "lens", "lo", "status"):
         assert bad(**{name: None}) == NULL, name
     assert bad(B=2 ** 31 - 1, C=2 ** 31 - 1, Hkv=2 ** 16) == OVERFLOW
+    assert bad(C=0, t=0, d=2 ** 29) == OVERFLOW  # empty, but no row is that wide
     assert bad(B=0, kc=None) == OK
 
 
@@ -133,6 +134,8 @@ def test_evict_refusals(gqa):
     assert bad(Co=9) == SHAPE                                  # in place, other capacity
     assert bad(ko=other, vo=other, wo=other, C=2 ** 31 - 1) == UNSUPPORTED
     assert bad(B=2 ** 31 - 1, C=2 ** 31 - 1, Hkv=2 ** 16) == OVERFLOW
+    assert bad(C=0, Co=0, budget=0, recent=0, d=2 ** 29) == OVERFLOW
+    assert bad(B=2 ** 20, Hkv=2 ** 12, C=0, Co=0, budget=0, recent=0) == UNSUPPORTED  # grids
     assert bad(B=0, kc=None) == OK
 
 
