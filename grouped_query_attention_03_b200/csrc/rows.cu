@@ -160,17 +160,29 @@ gqa_status launch_weigh_tc(const Params &p, const DeviceInfo &di, cudaStream_t s
                                         K::SMEM, st, mq, mk, p));
 }
 
-template <typename T>
-gqa_status launch_simt(const Params &p, const DeviceInfo &di, cudaStream_t st) {
+template <typename T, int RPT>
+gqa_status launch_simt_rpt(const Params &p, const DeviceInfo &di, cudaStream_t st) {
   const int64_t grid = (int64_t)p.B * p.Hkv * p.MG * p.ns;
   if (grid > INT_MAX) return GQA_ERR_UNSUPPORTED;
   static bool done[64] = {};
-  gqa_status s = allow_smem(gqa::rows::rows_simt_kernel<T>, gqa::rows::simt_smem(GQA_MAX_HEAD_DIM),
-                            di.id, done);
+  gqa_status s = allow_smem(gqa::rows::rows_simt_kernel<T, RPT>,
+                            gqa::rows::simt_smem(GQA_MAX_HEAD_DIM, sizeof(T)), di.id, done);
   if (s != GQA_OK) return s;
-  return launched(gqa::launch_dependent(gqa::rows::rows_simt_kernel<T>, dim3((unsigned)grid),
-                                        dim3(gqa::rows::kSimtThreads), gqa::rows::simt_smem(p.d),
-                                        st, p));
+  return launched(gqa::launch_dependent(gqa::rows::rows_simt_kernel<T, RPT>, dim3((unsigned)grid),
+                                        dim3(gqa::rows::kSimtThreads),
+                                        gqa::rows::simt_smem(p.d, sizeof(T)), st, p));
+}
+
+template <typename T>
+gqa_status launch_simt(Params p, const DeviceInfo &di, cudaStream_t st) {
+  p.vec = p.d * (int)sizeof(T) % 16 == 0 && aligned16(p.k) && aligned16(p.v) && aligned16(p.kd) &&
+          aligned16(p.vd);
+  switch (gqa::rows::simt_rpt(p.d)) {
+    case 1: return launch_simt_rpt<T, 1>(p, di, st);
+    case 2: return launch_simt_rpt<T, 2>(p, di, st);
+    case 4: return launch_simt_rpt<T, 4>(p, di, st);
+    default: return launch_simt_rpt<T, 8>(p, di, st);
+  }
 }
 
 // One row per sequence on the decode kernel, scores and statistics kept.

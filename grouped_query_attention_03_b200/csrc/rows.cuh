@@ -51,6 +51,7 @@ struct Params {
   int MG;                   // groups of group_rows rows per lane
   int ctas, pad;            // tensor-core split (ctas CTAs share all tiles)
   int ns;                   // CUDA-core split (ns parts per lane), else 0
+  int vec;                  // CUDA cores: rows are whole aligned 16-byte vectors
   int finish;               // rows_finish_kernel merges
   float scale_log2;
 };

@@ -3,12 +3,13 @@
 // head widths that the tensor-core kernel is not compiled for.
 //
 // CTA = (part, group of 16 rows, lane): the lane's keys (cells, then drafts)
-// are cut into ns equal parts.  32 keys at a time pass through shared
-// memory as fp32: each thread scores one key against 4 rows (the key's
-// features in its registers' reach, the rows' broadcast), the 4 warps run
-// the online softmax of 4 rows each, lane = key, and each thread mixes the
-// values of up to 2 columns for all 16 rows.  Bound by shared-memory reads:
-// 5 per 16 FMAs in both products.
+// are cut into ns equal parts, taken 32 at a time.  The 4 warps score 4 rows
+// each, lane = key (the key's features from its row in shared memory, the
+// rows' broadcast), and run their online softmax; then a thread mixes 4
+// columns of RPT rows.  Copies are asynchronous where rows are whole 16-byte
+// vectors: the next keys travel under the mix, the values under the scores.
+// Bound by shared-memory reads (8 cycles of them per 4 of FMAs in the scores, 5
+// in the mix) with many rows, by latency with few.
 #pragma once
 
 #include "rows.cuh"
@@ -19,20 +20,59 @@ namespace rows {
 constexpr int kSR = 16;  // rows per CTA
 constexpr int kSK = 32;  // keys per step
 constexpr int kSimtThreads = 128;
+constexpr int kSimtWarps = kSimtThreads / 32;
 
+// Row pitches: queries (floats) and keys or values (bytes).  4 words past a
+// multiple of 16 bytes keep a warp's rows in different banks.
 __host__ __device__ constexpr int simt_pitch(int d) { return ((d + 3) / 4) * 4 + 4; }
-inline int simt_smem(int d) { return (kSR + kSK) * simt_pitch(d) * 4 + kSK * kSR * 4; }
+__host__ __device__ constexpr int simt_kv_pitch(int d, int elem) {
+  return ((d + 3) / 4 * 4 * elem + 15) / 16 * 16 + 16;
+}
+inline int simt_smem(int d, int elem) {
+  return kSR * simt_pitch(d) * 4 + 2 * kSK * simt_kv_pitch(d, elem) + kSK * kSR * 4;
+}
 
+// Rows per thread in the mix: a thread per 4 columns and RPT rows.
+inline int simt_rpt(int d) { return d <= 32 ? 1 : d <= 64 ? 2 : d <= 128 ? 4 : 8; }
+
+// 4 elements of a row in shared memory.
 template <typename T>
+__device__ __forceinline__ float4 row4(const unsigned char *row, int c);
+template <>
+__device__ __forceinline__ float4 row4<float>(const unsigned char *row, int c) {
+  return *reinterpret_cast<const float4 *>(row + c * 16);
+}
+template <>
+__device__ __forceinline__ float4 row4<__nv_bfloat16>(const unsigned char *row, int c) {
+  const uint2 u = *reinterpret_cast<const uint2 *>(row + c * 8);
+  return make_float4(bf16lo_to_f32(u.x), bf16hi_to_f32(u.x), bf16lo_to_f32(u.y), bf16hi_to_f32(u.y));
+}
+
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <typename T, int RPT>
 __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const Params p) {
   extern __shared__ __align__(16) float sm[];
   __shared__ int32_t s_par[kMaxNodes];
-  __shared__ float s_alpha[kSR], s_ml[kSR][2];
+  __shared__ __align__(16) float s_alpha[kSR];
+  __shared__ float s_ml[kSR][2];
   __shared__ int s_last;
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
-  const int pitch = simt_pitch(p.d), d4 = (p.d + 3) / 4;
-  float *sq = sm, *skv = sq + kSR * pitch, *sp = skv + kSK * pitch;  // sp [key][row]
+  const int pitch = simt_pitch(p.d), kv_pitch = simt_kv_pitch(p.d, sizeof(T)), d4 = (p.d + 3) / 4;
+  float *sq = sm;
+  unsigned char *sk = reinterpret_cast<unsigned char *>(sq + kSR * pitch), *sv = sk + kSK * kv_pitch;
+  float *sp = reinterpret_cast<float *>(sv + kSK * kv_pitch);  // [key][row]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // blockIdx.x = (lane (b, g) * MG + group) * ns + part
   const long long L = (long long)blockIdx.x / p.ns;  // lane group
@@ -51,149 +91,203 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const Params p)
       for (int i = tid; i < nrows * p.d; i += kSimtThreads) o[i] = from_f32<T>(0.f);
     return;
   }
-  if (p.tree && p.parents)
-    for (int i = tid; i < p.t; i += kSimtThreads) s_par[i] = p.parents[(long long)b * p.t + i];
-  for (int i = tid; i < kSR * pitch; i += kSimtThreads) {
-    const int row = i / pitch, c = i - row * pitch;
-    sq[i] = (row < nrows && c < p.d) ? to_f32(((const T *)p.q)[(row0 + row) * p.d + c]) * p.scale_log2
-                                     : 0.f;
-  }
-  __syncthreads();
-  // this warp's 4 rows: what they may read
   const int lo0 = first_cell(p, n), nc = n - lo0;
   const int nkeys = nc + (p.tree ? p.t : 0);
-  int lo[4], hi[4];  // cells [lo, hi) of each row
-  Line line[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int row = warp * 4 + k, i = (rho0 + row) % p.t;
-    lo[k] = 0;
-    hi[k] = 0;
-    line[k].depth = -1;
-#pragma unroll
-    for (int w = 0; w < kMaxNodes / 32; ++w) line[k].bits[w] = 0u;
-    if (row >= nrows) continue;
-    if (p.tree) {
-      line[k] = line_of(p.parents ? s_par : nullptr, i, p.window);
-      if (line[k].refused && lane == 0) record_status(p.status, GQA_ERR_TREE);
-      if (line[k].depth >= 0) {
-        lo[k] = p.window > 0 ? max(0, n + line[k].depth - (p.window - 1)) : 0;
-        hi[k] = n;
-      }
-    } else {
-      hi[k] = n - p.t + i + 1;
-    }
-  }
   // keys [k0, k1) of the lane
   const int k0 = (int)((long long)nkeys * part / p.ns);
   const int k1 = (int)((long long)nkeys * (part + 1) / p.ns);
-  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, l[4] = {0.f, 0.f, 0.f, 0.f};
-  float acc[2][kSR];
-#pragma unroll
-  for (int c = 0; c < 2; ++c)
-#pragma unroll
-    for (int k = 0; k < kSR; ++k) acc[c][k] = 0.f;
-
-  // K (or V) rows of keys [kb, kb + 32) to shared memory; true if a value is
-  // not finite
-  auto stage = [&](const void *cache, const void *draft, int kb) -> bool {
-    bool odd = false;
-    for (int i = tid; i < kSK * pitch; i += kSimtThreads) {
-      const int key = i / pitch, c = i - key * pitch, kk = kb + key;
-      float x = 0.f;
-      if (kk < k1 && c < p.d) {
-        if (kk < nc)
-          x = to_f32(((const T *)cache)[(ln * p.C + lo0 + kk) * p.d + c]);
-        else
-          x = to_f32(((const T *)draft)[(ln * p.t + (kk - nc)) * p.d + c]);
-      }
-      odd |= !isfinite(x);
-      skv[i] = x;
-    }
-    return odd;
+  // rows of keys [kb, kb + 32) to shared memory; zeros behind k1
+  auto row_at = [&](const void *cache, const void *draft, int kk) {
+    return kk < nc ? (const T *)cache + (ln * p.C + lo0 + kk) * p.d
+                   : (const T *)draft + (ln * p.t + (kk - nc)) * p.d;
   };
-
-  for (int kb = k0; kb < k1; kb += kSK) {
-    __syncthreads();  // the last step's values and weights are used up
-    stage(p.k, p.kd, kb);
-    __syncthreads();
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    const float4 *k4 = reinterpret_cast<const float4 *>(skv + lane * pitch);
-    const float4 *q4 = reinterpret_cast<const float4 *>(sq + warp * 4 * pitch);
-    const int p4 = pitch / 4;
-    for (int c = 0; c < d4; ++c) {
-      const float4 kv = k4[c];
+  auto stage = [&](const void *cache, const void *draft, unsigned char *to, int kb) {
+    if (p.vec) {  // 16 bytes at a time, 1, 2 or 4 keys per warp
+      const int vpr = p.d * (int)sizeof(T) / 16;
+      const int kpw = vpr <= 8 ? 4 : vpr <= 16 ? 2 : 1, lpk = 32 / kpw;
+#pragma unroll 4
+      for (int key = warp * kpw + lane / lpk; key < kSK; key += kSimtWarps * kpw) {
+        const int kk = kb + key;
+        const T *src = row_at(cache, draft, min(kk, k1 - 1));
+        for (int e = lane % lpk; e < vpr; e += lpk)
+          cp_async16(to + key * kv_pitch + e * 16, reinterpret_cast<const unsigned char *>(src) + e * 16,
+                     kk < k1);
+      }
+    } else {
+      constexpr int U = kSK / kSimtWarps;
+      for (int c = lane; c < d4 * 4; c += 32) {
+        T x[U];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float4 qv = q4[k * p4 + c];
-        s[k] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, s[k]))));
+        for (int u = 0; u < U; ++u) {
+          const int kk = kb + warp + u * kSimtWarps;
+          x[u] = kk < k1 && c < p.d ? row_at(cache, draft, kk)[c] : from_f32<T>(0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          reinterpret_cast<T *>(to + (warp + u * kSimtWarps) * kv_pitch)[c] = x[u];
       }
     }
-    const int kk = kb + lane, cell = lo0 + kk, node = kk - nc;
+    cp_async_commit();
+  };
+  if (k0 < k1) {
+    stage(p.k, p.kd, sk, k0);
+    stage(p.v, p.vd, sv, k0);
+  }
+  if (p.tree && p.parents)
+    for (int i = tid; i < p.t; i += kSimtThreads) s_par[i] = p.parents[(long long)b * p.t + i];
+  for (int c = lane; c < pitch; c += 32) {
+    float x[kSR / kSimtWarps];
+#pragma unroll
+    for (int u = 0; u < kSR / kSimtWarps; ++u) {
+      const int row = warp + u * kSimtWarps;
+      x[u] = row < nrows && c < p.d ? to_f32(((const T *)p.q)[(row0 + row) * p.d + c]) * p.scale_log2 : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < kSR / kSimtWarps; ++u) sq[(warp + u * kSimtWarps) * pitch + c] = x[u];
+  }
+  for (int i = tid; i < kSK * kSR; i += kSimtThreads) sp[i] = 0.f;  // rows past the last stay 0
+  if (tid < kSR) {
+    s_alpha[tid] = 0.f;
+    s_ml[tid][0] = -INFINITY;
+    s_ml[tid][1] = 0.f;
+  }
+  __syncthreads();
+  // this warp's 4 rows: what they may read.  A lane works out row lane % 4.
+  int lo[4], hi[4];  // cells [lo, hi) of each row
+  uint32_t bits[4][kMaxNodes / 32];
+  {
+    const int row = warp * 4 + (lane & 3), i = (rho0 + row) % p.t;
+    Line ln4;
+    ln4.depth = -1;
+    ln4.refused = false;
+#pragma unroll
+    for (int w = 0; w < kMaxNodes / 32; ++w) ln4.bits[w] = 0u;
+    int lo1 = 0, hi1 = 0;
+    if (row < nrows) {
+      if (p.tree) {
+        ln4 = line_of(p.parents ? s_par : nullptr, i, p.window);
+        if (ln4.refused) record_status(p.status, GQA_ERR_TREE);
+        if (ln4.depth >= 0) {
+          lo1 = p.window > 0 ? max(0, n + ln4.depth - (p.window - 1)) : 0;
+          hi1 = n;
+        }
+      } else {
+        hi1 = n - p.t + i + 1;
+      }
+    }
+    __syncwarp();
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      bool ok = kk < k1;
-      if (kk < nc) {
-        ok = ok && cell >= lo[k] && cell < hi[k];
-      } else {
-        uint32_t word = 0u;
+      lo[k] = __shfl_sync(0xffffffffu, lo1, k);
+      hi[k] = __shfl_sync(0xffffffffu, hi1, k);
 #pragma unroll
-        for (int w = 0; w < kMaxNodes / 32; ++w)
-          if ((node >> 5) == w) word = line[k].bits[w];
-        ok = ok && ((word >> (node & 31)) & 1u);
-      }
-      if (!ok) s[k] = -INFINITY;
-      const int rho = rho0 + warp * 4 + k;
-      if (p.scores && kk < k1 && warp * 4 + k < nrows)
-        p.scores[(ln * p.R + rho) * p.Cp + cell] = s[k];
-      float mx = s[k];
-#pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-      const float m_new = fmaxf(m[k], mx);
-      const float msub = m_new == -INFINITY ? 0.f : m_new;
-      const float alpha = exp2f(m[k] - msub);  // 0 from -inf
-      const float pv = exp2f(s[k] - msub);
-      float ps = pv;
-#pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, off);
-      l[k] = fmaf(l[k], alpha, ps);
-      m[k] = m_new;
-      sp[lane * kSR + warp * 4 + k] = pv;
-      if (lane == 0) s_alpha[warp * 4 + k] = alpha;
+      for (int w = 0; w < kMaxNodes / 32; ++w) bits[k][w] = __shfl_sync(0xffffffffu, ln4.bits[w], k);
     }
-    __syncthreads();  // scores taken from skv; sp, s_alpha complete
-    // a value that is not finite must not reach rows that may not read it
-    const bool odd = __syncthreads_or(stage(p.v, p.vd, kb)) != 0;
-    float al[kSR];
+  }
+  const bool warp_on = warp * 4 < nrows;
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, l[4] = {0.f, 0.f, 0.f, 0.f};
+  // this thread's part of the mix: columns [4 cg, 4 cg + 4) of rows [mr, mr + RPT)
+  const int cg = tid % d4, mr = tid / d4 * RPT;
+  const bool mixes = mr < nrows;  // (kSR / RPT groups of rows at most have threads: mr < kSR there)
+  float acc[RPT][4];
 #pragma unroll
-    for (int k = 0; k < kSR; ++k) al[k] = s_alpha[k];
+  for (int k = 0; k < RPT; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
+
+  for (int kb = k0; kb < k1; kb += kSK) {
+    if (kb == k0)
+      cp_async_wait<1>();  // the keys (the values were asked for behind them)
+    else
+      cp_async_wait<0>();
+    __syncthreads();  // keys here; the last step's values and weights are used up
+    if (kb > k0) stage(p.v, p.vd, sv, kb);
+    if (warp_on) {
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      const unsigned char *krow = sk + lane * kv_pitch;
+      const float4 *q4 = reinterpret_cast<const float4 *>(sq + warp * 4 * pitch);
+      const int p4 = pitch / 4;
+#pragma unroll 4
+      for (int c = 0; c < d4; ++c) {
+        const float4 kv = row4<T>(krow, c);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int col = tid + c * kSimtThreads;
-      if (col >= p.d) continue;
-#pragma unroll
-      for (int k = 0; k < kSR; ++k) acc[c][k] *= al[k];
-      for (int key = 0; key < kSK; ++key) {
-        const float v = skv[key * pitch + col];
-        const float4 *w4 = reinterpret_cast<const float4 *>(sp + key * kSR);
-        float w[kSR];
-#pragma unroll
-        for (int k = 0; k < kSR / 4; ++k) {
-          const float4 y = w4[k];
-          w[4 * k] = y.x; w[4 * k + 1] = y.y; w[4 * k + 2] = y.z; w[4 * k + 3] = y.w;
+        for (int k = 0; k < 4; ++k) {
+          const float4 qv = q4[k * p4 + c];
+          s[k] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, s[k]))));
         }
-        if (odd) {
+      }
+      const int kk = kb + lane, cell = lo0 + kk, node = kk - nc;
+      float mx[4], ps[4];
 #pragma unroll
-          for (int k = 0; k < kSR; ++k)
-            if (w[k] != 0.f) acc[c][k] = fmaf(w[k], v, acc[c][k]);
+      for (int k = 0; k < 4; ++k) {
+        bool ok = kk < k1;
+        if (kk < nc) {
+          ok = ok && cell >= lo[k] && cell < hi[k];
         } else {
+          uint32_t word = 0u;
 #pragma unroll
-          for (int k = 0; k < kSR; ++k) acc[c][k] = fmaf(w[k], v, acc[c][k]);
+          for (int w = 0; w < kMaxNodes / 32; ++w)
+            if ((node >> 5) == w) word = bits[k][w];
+          ok = ok && ((word >> (node & 31)) & 1u);
+        }
+        if (!ok) s[k] = -INFINITY;
+        if (p.scores && kk < k1 && warp * 4 + k < nrows)
+          p.scores[(ln * p.R + rho0 + warp * 4 + k) * p.Cp + cell] = s[k];
+        mx[k] = s[k];
+      }
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], off));
+      float alpha[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float m_new = fmaxf(m[k], mx[k]);
+        const float msub = m_new == -INFINITY ? 0.f : m_new;
+        alpha[k] = exp2f(m[k] - msub);  // 0 from -inf
+        ps[k] = exp2f(s[k] - msub);
+        m[k] = m_new;
+      }
+      *reinterpret_cast<float4 *>(sp + lane * kSR + warp * 4) = make_float4(ps[0], ps[1], ps[2], ps[3]);
+      if (lane == 0)
+        *reinterpret_cast<float4 *>(s_alpha + warp * 4) =
+            make_float4(alpha[0], alpha[1], alpha[2], alpha[3]);
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ps[k] += __shfl_xor_sync(0xffffffffu, ps[k], off);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) l[k] = fmaf(l[k], alpha[k], ps[k]);
+    }
+    cp_async_wait<0>();
+    __syncthreads();  // values here; keys used up; sp and s_alpha complete
+    if (kb + kSK < k1) stage(p.k, p.kd, sk, kb + kSK);
+    if (mixes) {
+#pragma unroll
+      for (int k = 0; k < RPT; ++k) {
+        const float al = s_alpha[mr + k];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[k][j] *= al;
+      }
+#pragma unroll 4
+      for (int key = 0; key < kSK; ++key) {
+        const float4 v = row4<T>(sv + key * kv_pitch, cg);
+#pragma unroll
+        for (int k = 0; k < RPT; ++k) {
+          // (a weight of 0 adds nothing, whatever the value: a row's masked
+          // keys may hold what is not finite)
+          const float w = sp[key * kSR + mr + k];
+          if (w != 0.f) {
+            acc[k][0] = fmaf(w, v.x, acc[k][0]);
+            acc[k][1] = fmaf(w, v.y, acc[k][1]);
+            acc[k][2] = fmaf(w, v.z, acc[k][2]);
+            acc[k][3] = fmaf(w, v.w, acc[k][3]);
+          }
         }
       }
     }
   }
-  if (lane == 0) {
+  // Never leave a copy in flight into an exiting CTA.
+  cp_async_wait<0>();
+  if (lane == 0 && warp_on) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       s_ml[warp * 4 + k][0] = m[k];
@@ -208,35 +302,30 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const Params p)
           make_float2(mk == -INFINITY ? 0.f : mk, lk == 0.f ? 0.f : 1.f / lk);
     }
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int col = tid + c * kSimtThreads;
-      if (col >= p.d) continue;
+    for (int k = 0; k < RPT; ++k) {
+      if (mr + k >= nrows) break;
+      const float lk = s_ml[mr + k][1];
 #pragma unroll
-      for (int k = 0; k < kSR; ++k) {
-        if (k >= nrows) continue;
-        const float lk = s_ml[k][1];
-        o[(long long)k * p.d + col] = from_f32<T>(lk == 0.f ? 0.f : acc[c][k] / lk);  // 0: no keys
-      }
+      for (int j = 0; j < 4; ++j)
+        if (cg * 4 + j < p.d)  // 0: no keys
+          o[(long long)(mr + k) * p.d + cg * 4 + j] = from_f32<T>(lk == 0.f ? 0.f : acc[k][j] / lk);
     }
     return;
   }
   if (tid < nrows) p.ml[slot * kSR + tid] = make_float2(s_ml[tid][0], s_ml[tid][1]);
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const int col = tid + c * kSimtThreads;
-    if (col >= p.d) continue;
-#pragma unroll
-    for (int k = 0; k < kSR; ++k)
-      if (k < nrows) p.acc[((slot * d4 + col / 4) * kSR + k) * 4 + (col & 3)] = acc[c][k];
-  }
+  for (int k = 0; k < RPT; ++k)
+    if (mr + k < nrows)
+      *reinterpret_cast<float4 *>(p.acc + ((slot * d4 + cg) * kSR + mr + k) * 4) =
+          make_float4(acc[k][0], acc[k][1], acc[k][2], acc[k][3]);
   __syncthreads();
   if (tid == 0) s_last = count_part(&p.counters[L], p.ns);
   __syncthreads();
   if (!s_last) return;
-  merge_parts<kSimtThreads / 32>(p, L * p.ns, p.ns, nrows, warp, sm, pitch,
+  merge_parts<kSimtWarps>(p, L * p.ns, p.ns, nrows, warp, sm, pitch,
                                  p.lse ? p.lse + ln * p.R + rho0 : nullptr);
   __syncthreads();
-  for (int k = warp; k < nrows; k += kSimtThreads / 32)
+  for (int k = warp; k < nrows; k += kSimtWarps)
     for (int c = lane; c < p.d; c += 32) o[(long long)k * p.d + c] = from_f32<T>(sm[k * pitch + c]);
 }
 
