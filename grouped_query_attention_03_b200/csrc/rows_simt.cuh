@@ -3,13 +3,15 @@
 // head widths that the tensor-core kernel is not compiled for.
 //
 // CTA = (part, group of 16 rows, lane): the lane's keys (cells, then drafts)
-// are cut into ns equal parts, taken 32 at a time.  The 4 warps score 4 rows
-// each, lane = key (the key's features from its row in shared memory, the
-// rows' broadcast), and run their online softmax; then a thread mixes 4
-// columns of RPT rows.  Copies are asynchronous where rows are whole 16-byte
-// vectors: the next keys travel under the mix, the values under the scores.
+// are cut into ns equal parts, taken 32 at a time.  A warp scores 4 rows, lane =
+// key (the key's features from its row in shared memory, the rows' broadcast),
+// and runs their online softmax; then a thread mixes 4 columns of RPT rows.
+// With 8 rows or fewer the warps share a row group's features, and the threads
+// without rows of their own take a share of the keys in the mix.  Rows of
+// whole 16-byte vectors arrive by asynchronous copies: the next keys travel
+// under the mix, the values under the scores.
 // Bound by shared-memory reads (8 cycles of them per 4 of FMAs in the scores, 5
-// in the mix) with many rows, by latency with few.
+// in the mix) with many rows, by the latency of a step with few.
 #pragma once
 
 #include "rows.cuh"
@@ -48,11 +50,9 @@ __device__ __forceinline__ float4 row4<__nv_bfloat16>(const unsigned char *row, 
   return make_float4(bf16lo_to_f32(u.x), bf16hi_to_f32(u.x), bf16lo_to_f32(u.y), bf16hi_to_f32(u.y));
 }
 
-// 16 bytes to shared memory, or zeros.
-__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
-               "r"(on ? 16 : 0)
-               : "memory");
+// 16 bytes to shared memory.
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -60,11 +60,33 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// RPT weights, at an address of as many floats.
+template <int RPT>
+__device__ __forceinline__ void load_weights(const float *at, float *w) {
+  if constexpr (RPT >= 4) {
+#pragma unroll
+    for (int k = 0; k < RPT; k += 4) {
+      const float4 y = *reinterpret_cast<const float4 *>(at + k);
+      w[k] = y.x;
+      w[k + 1] = y.y;
+      w[k + 2] = y.z;
+      w[k + 3] = y.w;
+    }
+  } else if constexpr (RPT == 2) {
+    const float2 y = *reinterpret_cast<const float2 *>(at);
+    w[0] = y.x;
+    w[1] = y.y;
+  } else {
+    w[0] = at[0];
+  }
+}
+
 template <typename T, int RPT>
 __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const Params p) {
   extern __shared__ __align__(16) float sm[];
   __shared__ int32_t s_par[kMaxNodes];
   __shared__ __align__(16) float s_alpha[kSR];
+  __shared__ float4 s_part[kSimtWarps][kSK];
   __shared__ float s_ml[kSR][2];
   __shared__ int s_last;
   griddep_wait();
@@ -85,6 +107,16 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const Params p)
   const int n = p.seq_lens[b];
   T *o = (T *)p.o + row0 * p.d;
   const long long slot = L * p.ns + part;
+  for (int c = lane; c < pitch; c += 32) {  // (does not wait for the length)
+    float x[kSR / kSimtWarps];
+#pragma unroll
+    for (int u = 0; u < kSR / kSimtWarps; ++u) {
+      const int row = warp + u * kSimtWarps;
+      x[u] = row < nrows && c < p.d ? to_f32(((const T *)p.q)[(row0 + row) * p.d + c]) * p.scale_log2 : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < kSR / kSimtWarps; ++u) sq[(warp + u * kSimtWarps) * pitch + c] = x[u];
+  }
   if (!length_ok(p, n)) {
     if (tid == 0) record_status(p.status, GQA_ERR_CAPACITY);
     if (part == 0)
@@ -96,22 +128,25 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const Params p)
   // keys [k0, k1) of the lane
   const int k0 = (int)((long long)nkeys * part / p.ns);
   const int k1 = (int)((long long)nkeys * (part + 1) / p.ns);
-  // rows of keys [kb, kb + 32) to shared memory; zeros behind k1
-  auto row_at = [&](const void *cache, const void *draft, int kk) {
-    return kk < nc ? (const T *)cache + (ln * p.C + lo0 + kk) * p.d
-                   : (const T *)draft + (ln * p.t + (kk - nc)) * p.d;
-  };
+  // Rows of keys [kb, min(kb + 32, k1)) to shared memory.  What is behind them
+  // stays as it was: its scores are masked and its weights 0.
+  // LPK lanes of 16 bytes take a row (d > 128 in fp32: twice)
+  constexpr int LPK = RPT * (int)sizeof(T) >= 16 ? 32 : RPT * (int)sizeof(T) >= 8 ? 16 : 8;
+  const int v_key = tid / LPK, v_at = tid % LPK * 16, row_bytes = p.d * (int)sizeof(T);
   auto stage = [&](const void *cache, const void *draft, unsigned char *to, int kb) {
-    if (p.vec) {  // 16 bytes at a time, 1, 2 or 4 keys per warp
-      const int vpr = p.d * (int)sizeof(T) / 16;
-      const int kpw = vpr <= 8 ? 4 : vpr <= 16 ? 2 : 1, lpk = 32 / kpw;
-#pragma unroll 4
-      for (int key = warp * kpw + lane / lpk; key < kSK; key += kSimtWarps * kpw) {
+    if (p.vec) {
+      const char *c0 = (const char *)((const T *)cache + (ln * p.C + lo0) * p.d) + v_at;
+      const char *d0 = (const char *)((const T *)draft + ln * p.t * p.d) + v_at;
+#pragma unroll
+      for (int key = v_key; key < kSK; key += kSimtThreads / LPK) {
         const int kk = kb + key;
-        const T *src = row_at(cache, draft, min(kk, k1 - 1));
-        for (int e = lane % lpk; e < vpr; e += lpk)
-          cp_async16(to + key * kv_pitch + e * 16, reinterpret_cast<const unsigned char *>(src) + e * 16,
-                     kk < k1);
+        const char *src = kk < nc ? c0 + (long long)kk * row_bytes : d0 + (long long)(kk - nc) * row_bytes;
+        unsigned char *dst = to + key * kv_pitch + v_at;
+        if (kk < k1) {
+          if (v_at < row_bytes) cp_async16(dst, src);
+          if (RPT * sizeof(T) == 32 && v_at + LPK * 16 < row_bytes)
+            cp_async16(dst + LPK * 16, src + LPK * 16);
+        }
       }
     } else {
       constexpr int U = kSK / kSimtWarps;
@@ -120,7 +155,9 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const Params p)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int kk = kb + warp + u * kSimtWarps;
-          x[u] = kk < k1 && c < p.d ? row_at(cache, draft, kk)[c] : from_f32<T>(0.f);
+          x[u] = kk >= k1 || c >= p.d ? from_f32<T>(0.f)
+                 : kk < nc           ? ((const T *)cache)[(ln * p.C + lo0 + kk) * p.d + c]
+                                     : ((const T *)draft)[(ln * p.t + (kk - nc)) * p.d + c];
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -135,16 +172,6 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const Params p)
   }
   if (p.tree && p.parents)
     for (int i = tid; i < p.t; i += kSimtThreads) s_par[i] = p.parents[(long long)b * p.t + i];
-  for (int c = lane; c < pitch; c += 32) {
-    float x[kSR / kSimtWarps];
-#pragma unroll
-    for (int u = 0; u < kSR / kSimtWarps; ++u) {
-      const int row = warp + u * kSimtWarps;
-      x[u] = row < nrows && c < p.d ? to_f32(((const T *)p.q)[(row0 + row) * p.d + c]) * p.scale_log2 : 0.f;
-    }
-#pragma unroll
-    for (int u = 0; u < kSR / kSimtWarps; ++u) sq[(warp + u * kSimtWarps) * pitch + c] = x[u];
-  }
   for (int i = tid; i < kSK * kSR; i += kSimtThreads) sp[i] = 0.f;  // rows past the last stay 0
   if (tid < kSR) {
     s_alpha[tid] = 0.f;
@@ -152,11 +179,17 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const Params p)
     s_ml[tid][1] = 0.f;
   }
   __syncthreads();
-  // this warp's 4 rows: what they may read.  A lane works out row lane % 4.
+  // Warps per 4 rows: they share the rows' features, the first runs the softmax.
+  const int wpr = nrows <= 4 ? 4 : nrows <= 8 ? 2 : 1;
+  const int r4 = warp / wpr * 4, sub = warp & (wpr - 1);  // this warp's rows, its share
+  const int cw = (d4 + wpr - 1) / wpr, c_lo = min(d4, sub * cw), c_hi = min(d4, c_lo + cw);
+  const bool scores_on = r4 < nrows, softmax_on = scores_on && sub == 0;
+  // what the rows may read; a lane works out row lane % 4
   int lo[4], hi[4];  // cells [lo, hi) of each row
   uint32_t bits[4][kMaxNodes / 32];
-  {
-    const int row = warp * 4 + (lane & 3), i = (rho0 + row) % p.t;
+  int lo_all = 0, k_all = min(k1, nc);  // keys from cell lo_all to key k_all: all rows
+  if (softmax_on) {
+    const int row = r4 + (lane & 3), i = (rho0 + row) % p.t;
     Line ln4;
     ln4.depth = -1;
     ln4.refused = false;
@@ -182,13 +215,22 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const Params p)
       hi[k] = __shfl_sync(0xffffffffu, hi1, k);
 #pragma unroll
       for (int w = 0; w < kMaxNodes / 32; ++w) bits[k][w] = __shfl_sync(0xffffffffu, ln4.bits[w], k);
+      if (r4 + k < nrows) {
+        lo_all = max(lo_all, lo[k]);
+        k_all = min(k_all, hi[k] - lo0);
+      }
     }
   }
-  const bool warp_on = warp * 4 < nrows;
-  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, l[4] = {0.f, 0.f, 0.f, 0.f};
-  // this thread's part of the mix: columns [4 cg, 4 cg + 4) of rows [mr, mr + RPT)
-  const int cg = tid % d4, mr = tid / d4 * RPT;
-  const bool mixes = mr < nrows;  // (kSR / RPT groups of rows at most have threads: mr < kSR there)
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  float l[4] = {0.f, 0.f, 0.f, 0.f};  // this lane's keys
+  // This thread's part of the mix: columns [4 cg, 4 cg + 4) of rows [mr, mr +
+  // RPT), keys ks, ks + KS, ...
+  constexpr int G = kSR / RPT;  // groups of d4 threads: d4 G <= kSimtThreads
+  const int cg = tid % d4, mg = tid / d4;
+  int nrg = 1;  // groups of rows
+  while (nrg * RPT < nrows) nrg *= 2;
+  const int KS = G / nrg, ks = mg / nrg, mr = (mg & (nrg - 1)) * RPT;
+  const bool mixes = mg < G && mr < nrows;
   float acc[RPT][4];
 #pragma unroll
   for (int k = 0; k < RPT; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
@@ -200,13 +242,13 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const Params p)
       cp_async_wait<0>();
     __syncthreads();  // keys here; the last step's values and weights are used up
     if (kb > k0) stage(p.v, p.vd, sv, kb);
-    if (warp_on) {
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    if (scores_on) {
       const unsigned char *krow = sk + lane * kv_pitch;
-      const float4 *q4 = reinterpret_cast<const float4 *>(sq + warp * 4 * pitch);
+      const float4 *q4 = reinterpret_cast<const float4 *>(sq + r4 * pitch);
       const int p4 = pitch / 4;
 #pragma unroll 4
-      for (int c = 0; c < d4; ++c) {
+      for (int c = c_lo; c < c_hi; ++c) {
         const float4 kv = row4<T>(krow, c);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -214,48 +256,62 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const Params p)
           s[k] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, s[k]))));
         }
       }
-      const int kk = kb + lane, cell = lo0 + kk, node = kk - nc;
-      float mx[4], ps[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        bool ok = kk < k1;
-        if (kk < nc) {
-          ok = ok && cell >= lo[k] && cell < hi[k];
-        } else {
-          uint32_t word = 0u;
-#pragma unroll
-          for (int w = 0; w < kMaxNodes / 32; ++w)
-            if ((node >> 5) == w) word = bits[k][w];
-          ok = ok && ((word >> (node & 31)) & 1u);
+    }
+    if (wpr > 1) {
+      if (scores_on && sub > 0) s_part[warp][lane] = make_float4(s[0], s[1], s[2], s[3]);
+      __syncthreads();
+      if (softmax_on)
+        for (int u = 1; u < wpr; ++u) {
+          const float4 y = s_part[warp + u][lane];
+          s[0] += y.x;
+          s[1] += y.y;
+          s[2] += y.z;
+          s[3] += y.w;
         }
-        if (!ok) s[k] = -INFINITY;
-        if (p.scores && kk < k1 && warp * 4 + k < nrows)
-          p.scores[(ln * p.R + rho0 + warp * 4 + k) * p.Cp + cell] = s[k];
-        mx[k] = s[k];
+    }
+    if (softmax_on) {
+      const int kk = kb + lane, cell = lo0 + kk, node = kk - nc;
+      float mx[4], pv[4], alpha[4];
+      if (kb + kSK > k_all || lo0 + kb < lo_all) {  // some row may not read all of these keys
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          bool ok = kk < k1;
+          if (kk < nc) {
+            ok = ok && cell >= lo[k] && cell < hi[k];
+          } else {
+            uint32_t word = 0u;
+#pragma unroll
+            for (int w = 0; w < kMaxNodes / 32; ++w)
+              if ((node >> 5) == w) word = bits[k][w];
+            ok = ok && ((word >> (node & 31)) & 1u);
+          }
+          if (!ok) s[k] = -INFINITY;
+        }
       }
+      if (p.scores && kk < k1) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (r4 + k < nrows) p.scores[(ln * p.R + rho0 + r4 + k) * p.Cp + cell] = s[k];
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mx[k] = s[k];
 #pragma unroll
       for (int off = 16; off >= 1; off >>= 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], off));
-      float alpha[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float m_new = fmaxf(m[k], mx[k]);
         const float msub = m_new == -INFINITY ? 0.f : m_new;
         alpha[k] = exp2f(m[k] - msub);  // 0 from -inf
-        ps[k] = exp2f(s[k] - msub);
+        pv[k] = exp2f(s[k] - msub);
+        l[k] = fmaf(l[k], alpha[k], pv[k]);
         m[k] = m_new;
       }
-      *reinterpret_cast<float4 *>(sp + lane * kSR + warp * 4) = make_float4(ps[0], ps[1], ps[2], ps[3]);
+      *reinterpret_cast<float4 *>(sp + lane * kSR + r4) = make_float4(pv[0], pv[1], pv[2], pv[3]);
       if (lane == 0)
-        *reinterpret_cast<float4 *>(s_alpha + warp * 4) =
+        *reinterpret_cast<float4 *>(s_alpha + r4) =
             make_float4(alpha[0], alpha[1], alpha[2], alpha[3]);
-#pragma unroll
-      for (int off = 16; off >= 1; off >>= 1)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) ps[k] += __shfl_xor_sync(0xffffffffu, ps[k], off);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) l[k] = fmaf(l[k], alpha[k], ps[k]);
     }
     cp_async_wait<0>();
     __syncthreads();  // values here; keys used up; sp and s_alpha complete
@@ -268,30 +324,56 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const Params p)
         for (int j = 0; j < 4; ++j) acc[k][j] *= al;
       }
 #pragma unroll 4
-      for (int key = 0; key < kSK; ++key) {
+      for (int key = ks; key < kSK; key += KS) {
         const float4 v = row4<T>(sv + key * kv_pitch, cg);
+        float w[RPT];
+        load_weights<RPT>(sp + key * kSR + mr, w);
 #pragma unroll
-        for (int k = 0; k < RPT; ++k) {
-          // (a weight of 0 adds nothing, whatever the value: a row's masked
-          // keys may hold what is not finite)
-          const float w = sp[key * kSR + mr + k];
-          if (w != 0.f) {
-            acc[k][0] = fmaf(w, v.x, acc[k][0]);
-            acc[k][1] = fmaf(w, v.y, acc[k][1]);
-            acc[k][2] = fmaf(w, v.z, acc[k][2]);
-            acc[k][3] = fmaf(w, v.w, acc[k][3]);
+        for (int k = 0; k < RPT; ++k)
+          // a weight of 0 adds nothing, whatever the value: a row's masked keys
+          // may hold what is not finite
+          if (w[k] != 0.f) {
+            acc[k][0] = fmaf(w[k], v.x, acc[k][0]);
+            acc[k][1] = fmaf(w[k], v.y, acc[k][1]);
+            acc[k][2] = fmaf(w[k], v.z, acc[k][2]);
+            acc[k][3] = fmaf(w[k], v.w, acc[k][3]);
           }
-        }
       }
     }
   }
-  // Never leave a copy in flight into an exiting CTA.
-  cp_async_wait<0>();
-  if (lane == 0 && warp_on) {
+  __syncthreads();  // the queries and the last values are used up
+  if (KS > 1) {  // the shares of the keys, through the queries' place, in order
+    float *red = sq;
+    if (mixes && ks > 0)
+#pragma unroll
+      for (int k = 0; k < RPT; ++k)
+        *reinterpret_cast<float4 *>(red + ((mg * RPT + k) * d4 + cg) * 4) =
+            make_float4(acc[k][0], acc[k][1], acc[k][2], acc[k][3]);
+    __syncthreads();
+    if (mixes && ks == 0)
+      for (int u = 1; u < KS; ++u)
+#pragma unroll
+        for (int k = 0; k < RPT; ++k) {
+          const float4 y =
+              *reinterpret_cast<const float4 *>(red + (((u * nrg + mg) * RPT + k) * d4 + cg) * 4);
+          acc[k][0] += y.x;
+          acc[k][1] += y.y;
+          acc[k][2] += y.z;
+          acc[k][3] += y.w;
+        }
+  }
+  const bool writes = mixes && ks == 0;
+  if (softmax_on) {
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) l[k] += __shfl_xor_sync(0xffffffffu, l[k], off);
+  }
+  if (lane == 0 && softmax_on) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      s_ml[warp * 4 + k][0] = m[k];
-      s_ml[warp * 4 + k][1] = l[k];
+      s_ml[r4 + k][0] = m[k];
+      s_ml[r4 + k][1] = l[k];
     }
   }
   __syncthreads();
@@ -303,19 +385,19 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const Params p)
     }
 #pragma unroll
     for (int k = 0; k < RPT; ++k) {
-      if (mr + k >= nrows) break;
-      const float lk = s_ml[mr + k][1];
+      if (!writes || mr + k >= nrows) break;
+      const float lk = s_ml[mr + k][1], inv = lk == 0.f ? 0.f : 1.f / lk;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (cg * 4 + j < p.d)  // 0: no keys
-          o[(long long)(mr + k) * p.d + cg * 4 + j] = from_f32<T>(lk == 0.f ? 0.f : acc[k][j] / lk);
+          o[(long long)(mr + k) * p.d + cg * 4 + j] = from_f32<T>(lk == 0.f ? 0.f : acc[k][j] * inv);
     }
     return;
   }
   if (tid < nrows) p.ml[slot * kSR + tid] = make_float2(s_ml[tid][0], s_ml[tid][1]);
 #pragma unroll
   for (int k = 0; k < RPT; ++k)
-    if (mr + k < nrows)
+    if (writes && mr + k < nrows)
       *reinterpret_cast<float4 *>(p.acc + ((slot * d4 + cg) * kSR + mr + k) * 4) =
           make_float4(acc[k][0], acc[k][1], acc[k][2], acc[k][3]);
   __syncthreads();
