@@ -18,6 +18,10 @@ using gqa::rows::Params;
 // neither depends on the device.
 constexpr int kMaxCtas = 256;
 constexpr int kSimtCtas = 592;
+// Keys that a part of the CUDA-core kernel has at least (fp32, one head of 64, 44
+// nodes, 482 cells: 18.3 us with 64, 21.6 with 128; 16 groups of 4 rows over
+// 1000 cells: 26.5 and 22.6; in between elsewhere).
+constexpr int kPartKeys = 64;
 
 // What a lane group costs a CTA besides its tiles, in tiles (64 ragged
 // sequences, 63 nodes: 120 us with 2, 111 with 3 and with 4, 114 with 5).
@@ -81,9 +85,9 @@ bool layout(gqa_dtype dtype, int B, int Hq, int Hkv, int C, int d, int t, bool s
   } else {
     L.group_rows = gqa::rows::kSR;
     L.MG = (int)((R + gqa::rows::kSR - 1) / gqa::rows::kSR);
-    // parts of at least 64 keys, enough of them to fill the GPU
+    // parts of at least kPartKeys keys, enough of them to fill the GPU
     const int64_t groups = lanes * L.MG;
-    const int64_t most = std::max<int64_t>(1, ((int64_t)C + t) / 64);
+    const int64_t most = std::max<int64_t>(1, ((int64_t)C + t) / kPartKeys);
     L.ns = (int)std::min<int64_t>(std::min<int64_t>(most, 64),
                                   std::max<int64_t>(1, kSimtCtas / std::max<int64_t>(groups, 1)));
     L.slots = groups * L.ns;
@@ -288,6 +292,8 @@ gqa_status rows_impl(gqa_dtype dtype, const Operands &op, bool tree, int B, int 
   p.ctas = std::min(kMaxCtas, di.sms);
   p.pad = kPadTiles;
   p.ns = L.ns;
+  if (window > 0 && L.ns > 0)  // fewer parts where the window leaves few keys
+    p.ns = std::max(1, std::min(L.ns, (std::min(C, window - 1) + t) / kPartKeys));
   p.scale_log2 = scale * gqa::kLog2e;
   // the grids of the kernels that follow, checked before anything is launched
   const int row_blocks =

@@ -11,7 +11,11 @@
 // whole 16-byte vectors arrive by asynchronous copies: the next keys travel
 // under the mix, the values under the scores.
 // Bound by shared-memory reads (8 cycles of them per 4 of FMAs in the scores, 5
-// in the mix) with many rows, by the latency of a step with few.
+// in the mix) with many rows, by the latency of a step, about 1.5 us, with few.
+// fp32: 4 sequences of 2000 cells, 32 heads of 128 on 8, 32 nodes: 240 us, 18
+// TFLOP/s; one head, 58 cells, 2 nodes: 8.8 us.  Four CTAs per SM (128
+// registers) instead of as many as unlimited registers leave: 240 us against
+// 308 there, 8.8 against 8.6 here.
 #pragma once
 
 #include "rows.cuh"
@@ -82,7 +86,7 @@ __device__ __forceinline__ void load_weights(const float *at, float *w) {
 }
 
 template <typename T, int RPT>
-__global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const Params p) {
+__global__ void __launch_bounds__(kSimtThreads, 4) rows_simt_kernel(const Params p) {
   extern __shared__ __align__(16) float sm[];
   __shared__ int32_t s_par[kMaxNodes];
   __shared__ __align__(16) float s_alpha[kSR];
