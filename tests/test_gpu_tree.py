@@ -353,3 +353,30 @@ def test_one_workspace_with_the_other_decodes(cuda_lib):
             cuda_lib.decode_tree(q, kc, vc, kd, vd, pd, lt, out=o, workspace=w, stream=s)
     torch.cuda.synchronize()
     assert torch.equal(outs[0], alone[0]) and torch.equal(outs[1], alone[0])
+
+
+@pytest.mark.parametrize("d", [4, 20, 32, 33, 64, 80, 128, 200, 256])
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_cuda_core_rows_of_every_kind(cuda_lib, dtype, d):
+    """1 to 17 rows of a group (shared features, shared keys, two groups),
+    vectors and single elements, one part and several, windows."""
+    if dtype == BF and d in (64, 128):
+        shift = 1  # not 16-byte aligned: CUDA cores
+    else:
+        shift = 0
+    for r, t, lens, window in ((1, 1, [40], None), (3, 1, [0], None), (1, 5, [33], 7), (2, 4, [200], None),
+                               (3, 3, [95], 40), (4, 4, [31], None), (1, 17, [300], 21), (2, 40, [65], None)):
+        for off in {shift, 1}:
+            C = lens[0] + 3
+            ins = make(1, r, 1, C, d, t, lens, t + d, dtype)
+            par = random_tree(1, t, t + r, min(2, t - 1))
+            want, mag = so.tree(*[f64(x) for x in ins], par.numpy(), lens, window=window)
+            dev = []
+            for x in ins:
+                flat = torch.empty(x.numel() + off, dtype=dtype, device=DEV)[off:]
+                dev.append(flat.view(x.shape).copy_(x))
+            st = cuda_lib.new_status(DEV)
+            o = cuda_lib.decode_tree(*dev, par.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV),
+                                     window=window, status=st)
+            assert int(st.item()) == 0
+            assert_mix(o, want, mag, dtype, f"r{r} t{t} {lens} w{window} off{off}")
