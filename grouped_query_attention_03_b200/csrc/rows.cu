@@ -34,6 +34,11 @@ constexpr int kPadTiles = 3;
 // 1000 cells: 13.3 and 19.5).
 constexpr int kMergeRows = 800;
 
+// Parts that a warp of that kernel merges alone; more are shared by four (2 lanes
+// of 53 rows, 62 parts: 13.9 us with the attention, 24.3 alone; 2 of 256 rows, 74
+// parts: 30.1 and 35.5; but 8 lanes of 64 rows, 18 parts: 17.3 and 16.3).
+constexpr int kPartsPerWarp = 32;
+
 // Calls that share a workspace find each other's counters at the same place.
 static_assert(gqa::rows::kCounters == gqa::dec::kCtrFinish, "the counters' region");
 
@@ -42,6 +47,7 @@ struct Layout {
   bool dec = false;     // scored, one row: the decode kernel
   bool finish = false;  // the parts are merged by a kernel of their own
   bool scores = false;  // scored: the scores are kept, not multiplied again
+  int part_warps = 1;   // that share a lane group's parts in the merge
   int NT = 1, group_rows = 0, MG = 1, ns = 0, Cp = 0;
   int64_t slots = 0;
   size_t groups = 0, ml = 0, acc = 0, lse = 0, score_at = 0, total = 0;  // counters at 0
@@ -78,6 +84,7 @@ bool layout(gqa_dtype dtype, int B, int Hq, int Hkv, int C, int d, int t, bool s
     // Parts per lane group if all sequences are of one length, and their rows:
     // what the last CTA to count them would have to read.
     const int64_t parts = kMaxCtas / 2 / std::max<int64_t>(lanes * L.MG, 1) + 2;
+    L.part_warps = parts > kPartsPerWarp ? 4 : 1;
     L.finish = parts > gqa::rows::kAddParts || parts * L.group_rows > kMergeRows;
     // (8 lanes of 32768 cells, d = 128: 32 rows 53.8 us with the scores kept, 59.0
     // with the keys read again; 64 rows 74.6 and 60.5)
@@ -298,7 +305,7 @@ gqa_status rows_impl(gqa_dtype dtype, const Operands &op, bool tree, int B, int 
   // the grids of the kernels that follow, checked before anything is launched
   const int row_blocks =
       (std::min(L.group_rows, p.R) + gqa::rows::kFinishRows - 1) / gqa::rows::kFinishRows;
-  const int col_blocks = std::max(1, d / gqa::rows::kFinishCols);
+  const int col_blocks = std::max(1, d / (4 * gqa::rows::kFinishWarps / L.part_warps));
   const int64_t finish_blocks = (int64_t)B * Hkv * L.MG * row_blocks * col_blocks;
   if (L.finish && finish_blocks > INT_MAX) return GQA_ERR_UNSUPPORTED;
   const int cell_blocks = (C + gqa::rows::kWeighCells - 1) / gqa::rows::kWeighCells;
@@ -317,8 +324,9 @@ gqa_status rows_impl(gqa_dtype dtype, const Operands &op, bool tree, int B, int 
   }
   if (s != GQA_OK) return s;
   if (L.finish) {
-    s = launched(gqa::launch_dependent(gqa::rows::rows_finish_kernel<__nv_bfloat16>,
-                                       dim3((unsigned)finish_blocks),
+    auto *kernel = L.part_warps == 4 ? gqa::rows::rows_finish_kernel<__nv_bfloat16, 4>
+                                     : gqa::rows::rows_finish_kernel<__nv_bfloat16, 1>;
+    s = launched(gqa::launch_dependent(kernel, dim3((unsigned)finish_blocks),
                                        dim3(gqa::rows::kFinishThreads), 0, st, p, row_blocks, col_blocks));
     if (s != GQA_OK) return s;
   }

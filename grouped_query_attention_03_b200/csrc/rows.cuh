@@ -284,20 +284,26 @@ __device__ __forceinline__ void merge_parts(const Params &p, long long s0, int n
 }
 
 // ------------------------------------------------------------------- finish
-// Block (lane group, 32 rows, 8 groups of 4 columns): a warp has one group of
-// columns, a lane per row.  Up to 16 parts are fetched at once, their
-// statistics and sums together, so that the kernel is two round trips to L2
-// (which group, its parts); more parts take a pass over the statistics first.
+// Block (lane group, 32 rows, 8 / WP groups of 4 columns): WP warps share a group
+// of columns, each with every WP-th part, a lane per row.  Up to 16 parts are
+// fetched at once, their statistics and sums together, so that the kernel is
+// two round trips to L2 (which group, its parts); more parts per warp take a
+// pass over the statistics first.
 constexpr int kFinishThreads = 256;
-constexpr int kFinishRows = 32, kFinishCols = 32;
+constexpr int kFinishWarps = kFinishThreads / 32;
+constexpr int kFinishRows = 32;
 
-template <typename T>
+template <typename T, int WP>
 __global__ void __launch_bounds__(kFinishThreads)
     rows_finish_kernel(const Params p, int row_blocks, int col_blocks) {
-  __shared__ __align__(16) float tile[kFinishRows][kFinishCols + 4];
+  constexpr int WC = kFinishWarps / WP, COLS = 4 * WC;
+  __shared__ __align__(16) float tile[kFinishRows][COLS + 4];
+  __shared__ float4 s_acc[kFinishWarps][kFinishRows];
+  __shared__ float2 s_ml[kFinishWarps][kFinishRows];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int wc = warp / WP, wp = warp % WP;
   int i = blockIdx.x;
   const int cb = i % col_blocks;
   i /= col_blocks;
@@ -309,58 +315,83 @@ __global__ void __launch_bounds__(kFinishThreads)
   const int rho0 = grp * p.group_rows + rb * kFinishRows;  // first row of the lane
   const int nrows = min(min(kFinishRows, p.group_rows - rb * kFinishRows), p.R - rho0);
   if (nrows <= 0) return;
-  const int d4 = p.d / 4, c4 = cb * (kFinishCols / 4) + warp;  // d is 64 or 128
+  const int d4 = p.d / 4, c4 = cb * WC + wc;  // d is 64 or 128
+  float m = -INFINITY, l = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   if (lane < nrows) {
     const long long s0 = (long long)L + x.x;  // the first part's slot
     const int row = rb * kFinishRows + lane;
     const float2 *ml = p.ml + s0 * p.group_rows + row;
-    const float4 *acc = reinterpret_cast<const float4 *>(p.acc) + s0 * d4 * p.group_rows + row;
+    const float4 *acc =
+        reinterpret_cast<const float4 *>(p.acc) + (s0 * d4 + c4) * p.group_rows + row;
     constexpr int J = 16;
     const long long step = (long long)d4 * p.group_rows;
     float2 y[J];
     float4 v[J];
-    auto fetch = [&](int j0) {
+    auto fetch = [&](int j0) {  // parts j0, j0 + WP, ...
 #pragma unroll
       for (int j = 0; j < J; ++j)
-        if (j0 + j < np) {
-          y[j] = ml[(long long)(j0 + j) * p.group_rows];
-          v[j] = acc[(j0 + j) * step + (long long)c4 * p.group_rows];
+        if (j0 + j * WP < np) {
+          y[j] = ml[(long long)(j0 + j * WP) * p.group_rows];
+          v[j] = acc[(j0 + j * WP) * step];
         } else {
           y[j] = make_float2(-INFINITY, 0.f);
           v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
     };
-    fetch(0);
-    float m = -INFINITY;
+    fetch(wp);
 #pragma unroll
     for (int j = 0; j < J; ++j) m = fmaxf(m, y[j].x);
 #pragma unroll 16
-    for (int j = J; j < np; ++j) m = fmaxf(m, ml[(long long)j * p.group_rows].x);
-    float l = 0.f, a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-    for (int j0 = 0; j0 < np; j0 += J) {
-      if (j0 > 0) fetch(j0);
+    for (int j = wp + J * WP; j < np; j += WP) m = fmaxf(m, ml[(long long)j * p.group_rows].x);
+    for (int j0 = wp; j0 < np; j0 += J * WP) {
+      if (j0 > wp) fetch(j0);
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        if (j0 + j >= np) break;
+        if (j0 + j * WP >= np) break;
         const float e = part_weight(y[j], m);
         l = fmaf(e, y[j].y, l);
-        a0 = fmaf(e, v[j].x, a0);
-        a1 = fmaf(e, v[j].y, a1);
-        a2 = fmaf(e, v[j].z, a2);
-        a3 = fmaf(e, v[j].w, a3);
+        a.x = fmaf(e, v[j].x, a.x);
+        a.y = fmaf(e, v[j].y, a.y);
+        a.z = fmaf(e, v[j].z, a.z);
+        a.w = fmaf(e, v[j].w, a.w);
       }
     }
+  }
+  if constexpr (WP > 1) {  // the warps' sums, in order
+    s_ml[warp][lane] = make_float2(m, l);
+    s_acc[warp][lane] = a;
+    __syncthreads();
+    if (wp == 0) {
+#pragma unroll
+      for (int u = 1; u < WP; ++u) m = fmaxf(m, s_ml[warp + u][lane].x);
+      l = 0.f;
+      a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < WP; ++u) {
+        const float2 y = s_ml[warp + u][lane];
+        const float4 v = s_acc[warp + u][lane];
+        const float e = part_weight(y, m);
+        l = fmaf(e, y.y, l);
+        a.x = fmaf(e, v.x, a.x);
+        a.y = fmaf(e, v.y, a.y);
+        a.z = fmaf(e, v.z, a.z);
+        a.w = fmaf(e, v.w, a.w);
+      }
+    }
+  }
+  if (wp == 0 && lane < nrows) {
     const float inv = l == 0.f ? 0.f : 1.f / l;  // 0: no key at all
-    *reinterpret_cast<float4 *>(&tile[lane][warp * 4]) =
-        make_float4(a0 * inv, a1 * inv, a2 * inv, a3 * inv);
+    *reinterpret_cast<float4 *>(&tile[lane][wc * 4]) =
+        make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
     if (p.lse && c4 == 0)
       p.lse[(long long)ln * p.R + rho0 + lane] =
           make_float2(m == -INFINITY ? 0.f : m, l == 0.f ? 0.f : 1.f / l);
   }
   __syncthreads();
-  T *o = (T *)p.o + ((long long)ln * p.R + rho0) * p.d + cb * kFinishCols;
-  for (int e = threadIdx.x; e < nrows * (kFinishCols / 2); e += kFinishThreads) {
-    const int k = e / (kFinishCols / 2), col = 2 * (e % (kFinishCols / 2));
+  T *o = (T *)p.o + ((long long)ln * p.R + rho0) * p.d + cb * COLS;
+  for (int e = threadIdx.x; e < nrows * (COLS / 2); e += kFinishThreads) {
+    const int k = e / (COLS / 2), col = 2 * (e % (COLS / 2));
     *reinterpret_cast<uint32_t *>(o + (long long)k * p.d + col) =
         pack_bf16(tile[k][col], tile[k][col + 1]);
   }
