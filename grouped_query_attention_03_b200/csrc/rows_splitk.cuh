@@ -710,8 +710,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // columns of both O: o = O_0 a_0 + O_1 a_1, a_h = 2^(m_h - max)
       float m_all = m_run, l_all = l_run, a0 = 1.f, a1 = 0.f;
       if constexpr (NT == 1) {
-        // through the unused columns behind P in the last tile's S buffer
-        // (the next segment's first S goes to the other one)
+        // through the unused columns behind P in the last tile's S buffer.
+        // The next segment's first S goes to the other buffer; its second
+        // comes to this one, and the MMA lane holds it back until every warp
+        // is through here (o_free).
         const uint32_t tX = tmem + lane_base + s_buffer<NT>(jx - 1, x) * kTile + 32;
         tmem_st2(tX + wg * 64, m_run, l_run);
         tc::tmem_wait_st();
@@ -982,6 +984,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int j = sg.j0; ok && j < sg.j1; ++j, ++jj) {
             const int st = jj % K::STAGES;
             if (!mbar_wait(&sh.k_full[st], (jj / K::STAGES) & 1, &failed)) {
+              ok = false;
+              break;
+            }
+            // NT = 1: the second tile's S goes where the previous segment's
+            // softmax warps exchange their (m, l).  (They read no S before they
+            // are through with that, so nobody waits longer than before.)
+            if (NT == 1 && j == sg.j0 + 1 && sx[0] > 0 &&
+                !mbar_wait(&sh.o_free[0], (sx[0] - 1) & 1, &failed)) {
               ok = false;
               break;
             }
