@@ -310,7 +310,9 @@ __global__ void __launch_bounds__(kFinishThreads)
   const int rb = i % row_blocks, L = i / row_blocks;
   const int2 x = p.groups[L];
   const int ln = L / p.MG, grp = L - ln * p.MG, np = x.y;
-  if (!length_ok(p, p.seq_lens[ln / p.Hkv])) return;  // (its entry is not written)
+  // (A refused sequence's entry is not written; every other one is, also after
+  // a wait that ran out, since the writing warp walks on.)
+  if (!length_ok(p, p.seq_lens[ln / p.Hkv])) return;
   if (np < 2) return;
   const int rho0 = grp * p.group_rows + rb * kFinishRows;  // first row of the lane
   const int nrows = min(min(kFinishRows, p.group_rows - rb * kFinishRows), p.R - rho0);

@@ -281,7 +281,14 @@ __device__ __forceinline__ void tmem_ld2(uint32_t taddr, float &a, float &b) {
 
 // Whether any of the `threads` softmax threads says so (and a barrier).  The
 // end of the kernel has a barrier of its own: the second warpgroup may be
-// there while the first is still in a segment that is its alone.
+// there while the first is still in a segment that is its alone; and so has
+// such a segment (the first warpgroup's, 1), since a second warpgroup whose
+// wait ran out may be in a later one.
+// These barriers have no limit of their own.  They end because every warp
+// that takes part in one always comes to it: a warp whose wait ran out (its
+// later waits then return at once) skips its work and its arrivals, but walks
+// on through the same segments and barriers as the others, whose number
+// depends on nothing but the split and on what they agree on at a barrier.
 constexpr int kBarSegment = 3, kBarEnd = 4;
 __device__ __forceinline__ bool any_of_softmax(bool mine, int threads, int bar = kBarSegment) {
   uint32_t r;
@@ -494,8 +501,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int w = 0; w < 4; ++w) line.bits[w] = 0u;
     int jj = 0;                              // tiles of the range so far
     int jx = 0;                              // of these, with rows in this row tile
-    bool ok = true;
-    while (ok && walk.next(p, &sg)) {
+    // `failed` is the same for a warp's lanes wherever it is looked at
+    while (walk.next(p, &sg)) {  // (a warp that gave up walks on: see any_of_softmax)
       const int g = sg.vl / p.MG, grp = sg.vl - g * p.MG;
       const int rho_x = grp * p.group_rows + x * kM;   // the row tile's first row
       const int nx = min(NT, (p.R - grp * p.group_rows + kM - 1) / kM);  // row tiles here
@@ -545,7 +552,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         ? p.scores + (((long long)sg.b * p.Hkv + g) * p.R + rho) * p.Cp + e0
                         : nullptr;
       bool found = false;  // value rows cleared that are not finite
-      for (int j = sg.j0; j < sg.j1; ++j, ++jj, ++jx) {
+      int j = sg.j0;
+      for (; !failed && j < sg.j1; ++j, ++jj, ++jx) {
         const int sb = s_buffer<NT>(jx, x);
         const bool draft = j >= ncell_tiles;
         const int c0 = lo0 + j * kTile;  // first cell of the tile
@@ -553,7 +561,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const bool edge = draft || c0 + kTile > (p.tree ? sg.n : sg.n - p.t + 1) ||
                           (p.window > 0 && c0 < sg.n + p.t - p.window);
         if (!__all_sync(0xffffffffu, mbar_wait(&sh.s_full[sb], s_phase<NT>(jx), &failed))) {
-          ok = false;
+          failed = true;
           break;
         }
         tc::fence_after_sync();
@@ -584,7 +592,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           tc::fence_proxy_async_smem();
           if (!__all_sync(0xffffffffu, vok)) {
-            ok = false;
+            failed = true;
             break;
           }
         }
@@ -639,7 +647,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // O must hold P V of the previous tile before it is rescaled
             if (!__all_sync(0xffffffffu, mbar_wait(&sh.o_done[s_buffer<NT>(jx - 1, x)],
                                                    s_phase<NT>(jx - 1), &failed))) {
-              ok = false;
+              failed = true;
               break;
             }
             tc::fence_after_sync();
@@ -685,26 +693,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           l_run += lsum.x + lsum.y;
         }
       }
-      if (!ok) break;
+      jj += sg.j1 - j;  // (0 but after a wait that ran out)
+      jx += sg.j1 - j;
 
       // ---- the segment's end: O holds every P V once the last is done
-      if (!__all_sync(0xffffffffu, mbar_wait(&sh.o_done[s_buffer<NT>(jx - 1, x)],
-                                             s_phase<NT>(jx - 1), &failed))) {
-        ok = false;
-        break;
-      }
+      if (!failed && !__all_sync(0xffffffffu, mbar_wait(&sh.o_done[s_buffer<NT>(jx - 1, x)],
+                                                   s_phase<NT>(jx - 1), &failed)))
+        failed = true;
       tc::fence_after_sync();
       const bool whole = sg.j0 == 0 && sg.j1 == sg.ntiles;
       const int grow = x * kM + row;  // row within the group
       const long long orow = ((long long)sg.b * p.Hq + (long long)g * p.r) * p.t + rho;
       const int parties = NT == 1 ? 256 : 128 * nx;
-      if (any_of_softmax(found, parties)) {
-        if (warp_on)
+      const int bar = parties == 256 ? kBarSegment : 1;
+      const bool works = !failed && warp_on;
+      if (any_of_softmax(found, parties, bar)) {
+        if (works)
           add_unfinite<D>(p, sh, sg, mine, lo, hi, lo0, ncell_tiles, line, orow, m_run, tO, e0, e0 + NC);
-        any_of_softmax(false, parties);  // every row has read the list
+        any_of_softmax(false, parties, bar);  // every row has read the list
         if (threadIdx.x == 128)
           for (int k = 0; k < kUnfinite; ++k) sh.unfinite[k] = Unfinite{-1, {0u, 0u, 0u, 0u}};
-        any_of_softmax(false, parties);
+        any_of_softmax(false, parties, bar);
       }
       // NT = 1: the halves swap (m, l); each thread then combines d / 2
       // columns of both O: o = O_0 a_0 + O_1 a_1, a_h = 2^(m_h - max)
@@ -715,15 +724,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // comes to this one, and the MMA lane holds it back until every warp
         // is through here (o_free).
         const uint32_t tX = tmem + lane_base + s_buffer<NT>(jx - 1, x) * kTile + 32;
-        tmem_st2(tX + wg * 64, m_run, l_run);
-        tc::tmem_wait_st();
+        if (!failed) {
+          tmem_st2(tX + wg * 64, m_run, l_run);
+          tc::tmem_wait_st();
+        }
         tc::fence_before_sync();
-        any_of_softmax(false, parties);
+        any_of_softmax(false, parties, bar);
         tc::fence_after_sync();
-        float m0, l0, m1, l1;
-        tmem_ld2(tX, m0, l0);
-        tmem_ld2(tX + 64, m1, l1);
-        tc::tmem_wait_ld();
+        float m0 = -INFINITY, l0 = 0.f, m1 = -INFINITY, l1 = 0.f;
+        if (!failed) {
+          tmem_ld2(tX, m0, l0);
+          tmem_ld2(tX + 64, m1, l1);
+          tc::tmem_wait_ld();
+        }
         m_all = fmaxf(m0, m1);
         // (a half whose scores are all NaN has m = -inf and keeps its NaN sum)
         a0 = m0 == m_all ? 1.f : exp2f(m0 - m_all);
@@ -748,12 +761,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!whole && !is_e && !p.finish && !sh.aligned && gr.np <= kAddParts) {
         bool all = false;
         if (threadIdx.x == 128) all = ld_acquire_gpu(&p.counters[gr.c0]) == gr.np - 1;
-        add = any_of_softmax(all, parties);
+        add = any_of_softmax(all, parties, bar);
         if (add && threadIdx.x == 128) p.counters[gr.c0] = 0;
       }
       if (!whole && !add) {
         // partials as [column / 4][row][4]: a warp's 32 rows are 512 bytes
-        if (warp_on) {
+        if (works) {
           float4 *acc = reinterpret_cast<float4 *>(p.acc) +
                         ((gr.L + blockIdx.x) * (D / 4) + oc0 / 4) * p.group_rows + grow;
 #pragma unroll 1
@@ -773,12 +786,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           __syncwarp();
         }
         if (is_e) {
-          if (lane == 0) mbar_arrive(&sh.early_full);
+          if (!failed && lane == 0) mbar_arrive(&sh.early_full);
         } else if (!p.finish) {
-          any_of_softmax(false, parties);  // the part is written
+          any_of_softmax(false, parties, bar);  // the part is written
           bool last = false;
-          if (threadIdx.x == 128) last = count_part(&p.counters[gr.c0], gr.np);
-          add = any_of_softmax(last, parties);
+          if (!failed && threadIdx.x == 128) last = count_part(&p.counters[gr.c0], gr.np);
+          add = any_of_softmax(last, parties, bar);
           if (add && gr.np > kAddParts) {
             add = false;
             left = 1;
@@ -786,7 +799,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
       }
-      if ((whole || add) && warp_on) {
+      if ((whole || add) && works) {
         const float2 *ml = p.ml + (gr.L + gr.c0) * p.group_rows + min(grow, p.group_rows - 1);
         const int me = (int)blockIdx.x - gr.c0;
         float m_out = m_all, l_out = l_all;
@@ -858,17 +871,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.o_free[x]);
+      if (!failed && lane == 0) mbar_arrive(&sh.o_free[x]);
     }
     // Groups whose last part was counted here and could not be added above
     // are merged from the workspace, through the rings, which are empty by
     // now: every tile has been multiplied.  (The first warpgroup takes part in
     // every segment and speaks for both.)
-    if (any_of_softmax(ok && left, 256, kBarEnd)) merge_group<D>(p, sh.late, smem, warp - 4);
+    if (any_of_softmax(!failed && left, 256, kBarEnd)) merge_group<D>(p, sh.late, smem, warp - 4);
     Walk begin{sh.b, sh.vl, sh.off, sh.pad, sh.aligned, sh.start, sh.end, sh.len};
     if (begin.next(p, &sg) && is_early(p, sg, true, begin.pos < begin.end)) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&sh.early_done, 0, &failed))) ok = false;
-      if (any_of_softmax(ok && sh.early_last, 256, kBarEnd))
+      if (!__all_sync(0xffffffffu, mbar_wait(&sh.early_done, 0, &failed))) failed = true;
+      if (any_of_softmax(!failed && sh.early_last, 256, kBarEnd))
         merge_group<D>(p, group_of(p, sg, sh.per), smem, warp - 4);
     }
   } else {
@@ -900,7 +913,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const int ncell_tiles = sg.ntiles - p.tree, lo0 = first_cell(p, sg.n);
           const int ln = sg.b * p.Hkv + g;
           const int row0 = grp * p.group_rows;
-          if (segs == 0) load_q(segs++, nx, row0, ln);
+          if (segs == 0 && load_q(0, nx, row0, ln)) segs = 1;
           const bool q_due = jj > 0;
           for (int j = sg.j0; ok && j < sg.j1; ++j, ++jj) {
             const int st = jj % K::STAGES;
@@ -928,17 +941,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               tma_load_3d_hint(smem + K::OFF_V + st * K::TILE + c * K::BLK, mv, c * 64, c1, ln,
                                &sh.v_full[st], once);
             ++nv;
-            if (j == sg.j0 && q_due && !load_q(segs++, nx, row0, ln)) ok = false;
+            if (j == sg.j0 && q_due) {
+              ok = load_q(segs, nx, row0, ln);
+              segs += ok;
+            }
           }
         }
-        // Never leave a copy in flight into an exiting CTA.
-        bool f2 = false;
-        if (segs > 0) mbar_wait(&sh.q_full, (segs - 1) & 1, &f2);
+        // Never leave a copy in flight into an exiting CTA: each that was
+        // asked for is waited for, whatever became of the others.
+        auto landed = [&](uint64_t *bar, int parity) {
+          bool late = false;
+          mbar_wait(bar, parity, &late);
+          failed |= late;
+        };
+        if (segs > 0) landed(&sh.q_full, (segs - 1) & 1);
         for (int k = max(0, nk - K::STAGES); k < nk; ++k)
-          mbar_wait(&sh.k_full[k % K::STAGES], (k / K::STAGES) & 1, &f2);
+          landed(&sh.k_full[k % K::STAGES], (k / K::STAGES) & 1);
         for (int k = max(0, nv - K::STAGES); k < nv; ++k)
-          mbar_wait(&sh.v_full[k % K::STAGES], (k / K::STAGES) & 1, &f2);
-        failed |= f2;
+          landed(&sh.v_full[k % K::STAGES], (k / K::STAGES) & 1);
       }
     } else if (warp == 1) {
       // ================================================= MMA issuer

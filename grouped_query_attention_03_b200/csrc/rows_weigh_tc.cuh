@@ -180,10 +180,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const float masked = sc < 0.f ? INFINITY : -INFINITY;  // 2^(sc masked) = 0
     int step = 0, run = 0;
     bool ok = true;
-    while (ok && walk.next(p, &b, &g, &n, &j0, &j1)) {
+    // (a warp whose wait ran out skips its work but walks on through every
+    // run's barrier, which its fellows wait at without a limit)
+    while (walk.next(p, &b, &g, &n, &j0, &j1)) {
       const long long ln = (long long)b * p.Hkv + g;
       float *w = p.weights + ln * p.C;
-      for (int q = 0; ok && q < MQ; ++q, ++run) {
+      for (int q = 0; q < MQ; ++q, ++run) {
         const int rb = run & 1;
         // the rows' statistics (rows past the lane's: weight 0).  Written by
         // the first warpgroup; the buffer's last readers have passed the
@@ -195,7 +197,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           sh.inv[rb][key] = y.y;
         }
         any_of_softmax(false, 256);
-        for (int j = j0; j < j1; ++j, ++step) {
+        const int step_end = step + (j1 - j0);
+        for (int j = j0; ok && j < j1; ++j, ++step) {
           if ((step & 1) != wg) continue;
           const int sb = step & 3;
           const int cell = j * kTile + key;
@@ -241,6 +244,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           if (cell < n) w[cell] = old + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
         }
+        step = step_end;
       }
     }
   } else if (warp == 0) {
@@ -275,12 +279,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
       }
-      // Never leave a copy in flight into an exiting CTA.
-      bool f2 = false;
-      for (int k = max(0, nq - 2); k < nq; ++k) mbar_wait(&sh.q_full[k & 1], (k >> 1) & 1, &f2);
+      // Never leave a copy in flight into an exiting CTA: each that was asked
+      // for is waited for, whatever became of the others.
+      auto landed = [&](uint64_t *bar, int parity) {
+        bool late = false;
+        mbar_wait(bar, parity, &late);
+        failed |= late;
+      };
+      for (int k = max(0, nq - 2); k < nq; ++k) landed(&sh.q_full[k & 1], (k >> 1) & 1);
       for (int k = max(0, nk - K::STAGES); k < nk; ++k)
-        mbar_wait(&sh.k_full[k % K::STAGES], (k / K::STAGES) & 1, &f2);
-      failed |= f2;
+        landed(&sh.k_full[k % K::STAGES], (k / K::STAGES) & 1);
     }
   } else if (warp == 1) {
     if (lane == 0) {

@@ -1,17 +1,19 @@
-"""The barrier protocol of rows_splitk_kernel (the tensor-core kernel behind
-gqa_decode_tree and gqa_decode_scored), restated role by role and run in a
-simulator that knows what is ordered.  A change to the waits, arrivals or
-named barriers of the kernel belongs here too.
+"""The barrier protocols of rows_splitk_kernel and rows_weigh_tc_kernel (the
+tensor-core kernels behind gqa_decode_tree and gqa_decode_scored), restated
+role by role and run in a simulator that knows what is ordered and what may
+run out.  A change to the waits, arrivals or named barriers of a kernel
+belongs here too.
 
-Held: no two conflicting accesses to TMEM or shared memory are unordered.  A
-rule that the kernel keeps for this can be taken away here (never on a GPU),
-and the simulator then finds what it prevents."""
+Held: no two conflicting accesses to TMEM or shared memory are unordered; and
+a wait that runs out anywhere ends every role, none stays at a named barrier.
+Each rule that the kernels keep for this can be taken away here (never on a
+GPU), and the simulator then finds what it prevents."""
 import itertools
 import random
 
 import pytest
 
-from protocol_sim import Race, Sim, Waiter
+from protocol_sim import Hang, Race, Sim, Waiter
 
 STAGES = 3
 
@@ -281,6 +283,105 @@ def splitk(NT, segs, seed=0, lost=None, rush=0.0, second_waits=True, walks_on=Tr
     return sim
 
 
+def weigh(runs, seed=0, lost=None, rush=0.0, walks_on=True):
+    """runs: tiles of each run of the CTA (a lane's tiles, for 128 rows each)."""
+    bars = {"mma_fin": 1}
+    for s in range(2):
+        bars["q_full", s] = bars["q_empty", s] = 1
+    for s in range(4):
+        bars["k_full", s] = bars["k_empty", s] = bars["s_full", s] = 1
+        bars["s_empty", s] = 4
+    sim = Sim(bars, seed, rush)
+
+    def producer():
+        w = Waiter()
+        nq = nk = 0
+        ok = True
+        for tiles in runs:
+            if not ok or (nq >= 2 and not (yield from w.wait(("q_empty", nq & 1), (nq >> 1) - 1))):
+                break
+            yield ("write", ("Q", nq & 1))
+            if lost != ("q", nq):
+                yield ("arrive", ("q_full", nq & 1))
+            nq += 1
+            for _ in range(tiles):
+                st = nk & 3
+                if nk >= 4 and not (yield from w.wait(("k_empty", st), (nk >> 2) - 1)):
+                    ok = False
+                    break
+                yield ("write", ("K", st))
+                if lost != ("k", nk):
+                    yield ("arrive", ("k_full", st))
+                nk += 1
+        for k in range(max(0, nq - 2), nq):
+            yield from Waiter().wait(("q_full", k & 1), k >> 1)
+        for k in range(max(0, nk - 4), nk):
+            yield from Waiter().wait(("k_full", k & 3), k >> 2)
+        yield ("named", 0, 384, False)
+
+    def mma():
+        w = Waiter()
+        nq = step = 0
+        ok = True
+        for tiles in runs:
+            if not ok or not (yield from w.wait(("q_full", nq & 1), nq >> 1)):
+                break
+            for _ in range(tiles):
+                sb = step & 3
+                if not (yield from w.wait(("k_full", sb), step >> 2)) or \
+                        (step >= 4 and not (yield from w.wait(("s_empty", sb), (step >> 2) - 1))):
+                    ok = False
+                    break
+                yield ("mma", [("Q", nq & 1), ("K", sb)], [("S", sb, q) for q in range(4)])
+                yield ("commit", ("s_full", sb))
+                yield ("commit", ("k_empty", sb))
+                step += 1
+            yield ("commit", ("q_empty", nq & 1))
+            nq += 1
+        yield ("commit", "mma_fin")
+        yield from Waiter().wait("mma_fin", 0)
+        yield ("named", 0, 384, False)
+
+    def softmax(warp):
+        w = Waiter()
+        wg, q4 = warp >> 2, warp & 3
+        step = 0
+        ok = True
+        for run, tiles in enumerate(runs):
+            if not ok and not walks_on:
+                break
+            if wg == 0:
+                yield ("write", ("stats", run & 1, q4))
+            yield ("named", 3, 256, False)
+            for j in range(tiles):
+                s = step + j
+                if not ok or (s & 1) != wg:
+                    continue
+                yield ("read", ("w", j, q4))
+                if not (yield from w.wait(("s_full", s & 3), s >> 2)):
+                    ok = False
+                    break
+                yield ("read", ("S", s & 3, q4))
+                for q in range(4):
+                    yield ("read", ("stats", run & 1, q))
+                yield ("arrive", ("s_empty", s & 3))
+                yield ("write", ("w", j, q4))
+            step += tiles
+        yield ("named", 0, 384, False)
+
+    def idle():
+        yield ("named", 0, 384, False)
+
+    sim.add("producer", producer())
+    sim.add("mma", mma())
+    for k in range(2):
+        sim.add(f"idle{k}", idle())
+    for k in range(8):
+        sim.add(f"softmax{k}", softmax(k))
+    sim.run()
+    return sim
+
+
 def plans(NT):
     """Segments of 1 to 5 tiles, one to four of them, every kind of ends."""
     rng = random.Random(NT)
@@ -311,3 +412,47 @@ def test_the_second_tile_waits_for_the_exchanged_maxima():
         splitk(1, [Seg(1, kind="early"), Seg(5), Seg(3, kind="part")], second_waits=False)
     splitk(1, [Seg(4)], second_waits=False)             # one segment: nothing to wait for
     splitk(1, [Seg(4), Seg(1)], second_waits=False)     # one tile: the other buffer
+
+
+def lost_copies(segs):
+    tiles = sum(s.tiles for s in segs)
+    return [("q", k) for k in range(len(segs))] + [(c, k) for c in "kv" for k in range(tiles)]
+
+
+@pytest.mark.parametrize("NT", [1, 2])
+def test_a_wait_that_runs_out_ends_every_role(NT):
+    """A copy that never comes, and waits that give up on one that is late."""
+    rng = random.Random(7)
+    for segs in plans(NT):
+        for lost in rng.sample(lost_copies(segs), 2):
+            assert splitk(NT, segs, seed=rng.random(), lost=lost).gave_up, (segs, lost)
+        for rush in (0.002, 0.02):
+            splitk(NT, segs, seed=rng.random(), rush=rush)
+
+
+def hangs(runs, of, *args, **kw):
+    n = 0
+    for seed in range(runs):
+        try:
+            of(*args, seed=seed, **kw)
+        except Hang:
+            n += 1
+    return n
+
+
+def test_what_the_rules_for_it_prevent():
+    two = [Seg(3), Seg(2, kind="part")]
+    assert hangs(300, splitk, 1, two, rush=0.01, walks_on=False) > 0
+    assert hangs(300, splitk, 1, two, rush=0.01) == 0
+    mixed = [Seg(2, 1), Seg(2, 2), Seg(1, 1), Seg(3, 2)]
+    assert hangs(300, splitk, 2, mixed, rush=0.01, own_barrier=False) > 0
+    assert hangs(300, splitk, 2, mixed, rush=0.01) == 0
+
+
+def test_weights_from_the_keys():
+    for seed, runs in enumerate(itertools.product((1, 2, 3, 6), repeat=3)):
+        assert not weigh(runs, seed=seed).gave_up
+        for lost in [("q", 1), ("q", 2), ("k", 0), ("k", sum(runs) - 1), ("k", runs[0])]:
+            assert weigh(runs, seed=seed, lost=lost).gave_up, (runs, lost)
+    assert hangs(100, weigh, (3, 2, 2), rush=0.01, walks_on=False) > 0
+    assert hangs(100, weigh, (3, 2, 2), rush=0.01) == 0
