@@ -41,6 +41,7 @@ constexpr int kPartsPerWarp = 32;
 
 // Calls that share a workspace find each other's counters at the same place.
 static_assert(gqa::rows::kCounters == gqa::dec::kCtrFinish, "the counters' region");
+static_assert((gqa::rows::kCounters + 1) * sizeof(int) <= GQA_WORKSPACE_ZERO_BYTES, "what must be zero");
 
 struct Layout {
   bool tc = false;
@@ -62,7 +63,14 @@ bool layout(gqa_dtype dtype, int B, int Hq, int Hkv, int C, int d, int t, bool s
   if (!elems(&R, {Hq / Hkv, t}) || !elems(&rows, {B, Hq, t}) || !elems(&lanes, {B, Hkv}))
     return false;
   if (rows > INT_MAX / 2 || lanes > INT_MAX / 2) return false;
-  L.tc = tc_ok && dtype == GQA_BF16 && (d == 64 || d == 128);
+  const bool tc_type = dtype == GQA_BF16 && (d == 64 || d == 128);
+  L.tc = tc_ok && tc_type;
+  // With many rows the tensor-core kernel's scores are not kept but multiplied
+  // again (8 lanes of 32768 cells, d = 128: 32 rows 53.8 us with the scores kept,
+  // 59.0 with the keys read again; 64 rows 74.6 and 60.5).  Nor are they where
+  // the buffers' alignment sends such a call to CUDA cores, so that a workspace
+  // holds them only where they are always used.
+  L.scores = scored && !(tc_type && R > d / 4);
   // One scored row is a decode step: its kernel reads the cache at the same
   // rate and has a tenth of the tile kernel's fixed costs (B = 8, 8001 cells:
   // 59 us with tiles of 128 rows).
@@ -73,7 +81,7 @@ bool layout(gqa_dtype dtype, int B, int Hq, int Hkv, int C, int d, int t, bool s
     L.ml = D.ml;  // (counters at 0)
     L.acc = D.acc;
     L.lse = round256(D.total);
-    L.scores = true;
+    L.scores = true;  // (of one row each, whatever the group)
   } else if (L.tc) {
     // up to 128 rows fill one row tile; more are taken in pairs of tiles, so
     // that two share each K and V tile
@@ -86,9 +94,6 @@ bool layout(gqa_dtype dtype, int B, int Hq, int Hkv, int C, int d, int t, bool s
     const int64_t parts = kMaxCtas / 2 / std::max<int64_t>(lanes * L.MG, 1) + 2;
     L.part_warps = parts > kPartsPerWarp ? 4 : 1;
     L.finish = parts > gqa::rows::kAddParts || parts * L.group_rows > kMergeRows;
-    // (8 lanes of 32768 cells, d = 128: 32 rows 53.8 us with the scores kept, 59.0
-    // with the keys read again; 64 rows 74.6 and 60.5)
-    L.scores = scored && R <= d / 4;
   } else {
     L.group_rows = gqa::rows::kSR;
     L.MG = (int)((R + gqa::rows::kSR - 1) / gqa::rows::kSR);
@@ -98,7 +103,6 @@ bool layout(gqa_dtype dtype, int B, int Hq, int Hkv, int C, int d, int t, bool s
     L.ns = (int)std::min<int64_t>(std::min<int64_t>(most, 64),
                                   std::max<int64_t>(1, kSimtCtas / std::max<int64_t>(groups, 1)));
     L.slots = groups * L.ns;
-    L.scores = scored;
   }
   if (!L.dec) {
     int64_t n;
@@ -308,7 +312,8 @@ gqa_status rows_impl(gqa_dtype dtype, const Operands &op, bool tree, int B, int 
   const int col_blocks = std::max(1, d / (4 * gqa::rows::kFinishWarps / L.part_warps));
   const int64_t finish_blocks = (int64_t)B * Hkv * L.MG * row_blocks * col_blocks;
   if (L.finish && finish_blocks > INT_MAX) return GQA_ERR_UNSUPPORTED;
-  const int cell_blocks = (C + gqa::rows::kWeighCells - 1) / gqa::rows::kWeighCells;
+  const int per_block = L.scores ? gqa::rows::kWeighCells : gqa::rows::kWeighKeys;
+  const int cell_blocks = (C + per_block - 1) / per_block;
   const int64_t grid = tree ? 0 : (int64_t)B * Hkv * cell_blocks;
   if (grid > INT_MAX) return GQA_ERR_UNSUPPORTED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -331,13 +336,19 @@ gqa_status rows_impl(gqa_dtype dtype, const Operands &op, bool tree, int B, int 
     if (s != GQA_OK) return s;
   }
   if (tree) return s;
-  if (!L.scores) return d == 64 ? launch_weigh_tc<64>(p, di, st) : launch_weigh_tc<128>(p, di, st);
+  if (!L.scores && L.tc)
+    return d == 64 ? launch_weigh_tc<64>(p, di, st) : launch_weigh_tc<128>(p, di, st);
+  if (!L.scores)
+    return launched(gqa::launch_dependent(
+        d == 64 ? gqa::rows::rows_weigh_keys_kernel<64> : gqa::rows::rows_weigh_keys_kernel<128>,
+        dim3((unsigned)grid), dim3(gqa::rows::kWeighKeyThreads), 0, st, p, cell_blocks));
   return launched(gqa::launch_dependent(gqa::rows::rows_weigh_kernel, dim3((unsigned)grid),
                                         dim3(gqa::rows::kWeighThreads), 0, st, p, cell_blocks));
 }
 
 // The larger of the two layouts: buffers that are not 16-byte aligned run
-// the CUDA-core kernel.
+// the CUDA-core kernel.  (They are of like size: partial sums, and scores where
+// either keeps them.)
 size_t workspace_bytes_of(gqa_dtype dtype, int B, int Hq, int Hkv, int C, int d, int t, bool scored) {
   if (dtype != GQA_F32 && dtype != GQA_BF16) return 0;
   if (B < 0 || C < 0 || t < 0 || t > GQA_MAX_TREE || check_heads(Hq, Hkv, d) != GQA_OK) return 0;

@@ -19,7 +19,7 @@
 // scored: every row's m and 1 / l are kept, and a second kernel adds
 // sum_rho 2^(s - m_rho) / l_rho to each cell's weight: from the scores, left
 // in the workspace by the parts (rows_weigh_kernel), or from the keys, read
-// once more (rows_weigh_tc.cuh).
+// once more (rows_weigh_tc.cuh; rows_weigh_keys_kernel on CUDA cores).
 #pragma once
 
 #include "common.cuh"

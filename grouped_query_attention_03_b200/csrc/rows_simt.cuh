@@ -415,5 +415,67 @@ __global__ void __launch_bounds__(kSimtThreads, 4) rows_simt_kernel(const Params
     for (int c = lane; c < p.d; c += 32) o[(long long)k * p.d + c] = from_f32<T>(sm[k * pitch + c]);
 }
 
+// ------------------------------------------------------------------ weights
+// What each cell received, from the keys: for many scored rows of the bf16
+// types that the tensor-core kernel takes (which keeps no scores for them, see
+// rows_weigh_tc.cuh), in buffers that are not aligned for it.  The workspace
+// query does not know the alignment, so the scores are not kept here either.
+// Block = 64 cells of a lane, two threads per cell: its key in shared memory,
+// 16 rows' features and statistics at a time, 8 rows' products together in
+// each.  Bound by shared-memory reads, like the scores above (8 lanes of 32768
+// cells, 128 rows of 128: 1.91 ms with the attention, against 1.63 with 134 MB of
+// scores kept; 8 lanes of 2000, 64 rows of 64: 95 us and 69).
+constexpr int kWeighKeys = 64, kWeighRows = 16, kWeighKeyThreads = 2 * kWeighKeys;
+
+template <int D>
+__global__ void __launch_bounds__(kWeighKeyThreads) rows_weigh_keys_kernel(const Params p, int cell_blocks) {
+  constexpr int PITCH = 2 * D + 8;  // bytes: a warp's 8-byte reads meet no bank twice
+  __shared__ __align__(16) unsigned char keys[kWeighKeys * PITCH];
+  __shared__ __align__(16) float q[kWeighRows][D];
+  __shared__ float s_m[kWeighRows], s_inv[kWeighRows], s_w[kWeighKeys];
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const int tid = threadIdx.x, key = tid % kWeighKeys, k0 = tid / kWeighKeys * 8;
+  const long long ln = blockIdx.x / cell_blocks;
+  const int j0 = (int)(blockIdx.x - ln * cell_blocks) * kWeighKeys, cell = j0 + key;
+  const int b = (int)(ln / p.Hkv), n = p.seq_lens[b];
+  if (!length_ok(p, n) || j0 >= n) return;
+  const __nv_bfloat16 *k = (const __nv_bfloat16 *)p.k + (ln * p.C + j0) * D;
+  for (int i = tid; i < kWeighKeys * D; i += kWeighKeyThreads)
+    if (j0 + i / D < n) *reinterpret_cast<__nv_bfloat16 *>(keys + i / D * PITCH + i % D * 2) = k[i];
+  float w = 0.f;
+  for (int r0 = 0; r0 < p.R; r0 += kWeighRows) {
+    const int nr = min(kWeighRows, p.R - r0);
+    __syncthreads();
+    for (int i = tid; i < kWeighRows * D; i += kWeighKeyThreads)
+      q[i / D][i % D] =
+          i / D < nr ? to_f32(((const __nv_bfloat16 *)p.q)[(ln * p.R + r0) * D + i]) * p.scale_log2 : 0.f;
+    if (tid < nr) {
+      const float2 x = p.lse[ln * p.R + r0 + tid];
+      s_m[tid] = x.x;
+      s_inv[tid] = x.y;
+    }
+    __syncthreads();
+    if (cell >= n || k0 >= nr) continue;
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int c = 0; c < D / 4; ++c) {
+      const float4 kv = row4<__nv_bfloat16>(keys + key * PITCH, c);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float4 qv = *reinterpret_cast<const float4 *>(&q[k0 + u][c * 4]);
+        s[u] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, s[u]))));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)  // row i reads the cell if it is at or before its own
+      if (k0 + u < nr && cell <= n - p.t + (r0 + k0 + u) % p.t)
+        w = fmaf(exp2f(s[u] - s_m[k0 + u]), s_inv[k0 + u], w);
+  }
+  if (k0 > 0) s_w[key] = w;
+  __syncthreads();
+  if (k0 == 0 && cell < n) p.weights[ln * p.C + cell] += w + s_w[key];
+}
+
 }  // namespace rows
 }  // namespace gqa

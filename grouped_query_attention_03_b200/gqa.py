@@ -36,6 +36,7 @@ EXPORTS = ("gqa_prefill", "gqa_prefill_packed", "gqa_decode", "gqa_decode_worksp
 
 NOALLOC_SCRATCH_BYTES = 8 << 20  # GQA_NOALLOC_SCRATCH_BYTES in include/gqa.h
 MAX_TREE = 128  # GQA_MAX_TREE in include/gqa.h
+WORKSPACE_ZERO_BYTES = 4352  # GQA_WORKSPACE_ZERO_BYTES in include/gqa.h
 
 
 class GQAError(RuntimeError):
@@ -480,14 +481,23 @@ def qk_norm_rope(qkv, Hq, Hkv, d, *, q_weight=None, k_weight=None, eps=1e-6, inv
     return q, k, v
 
 
+def _workspace(n, device):
+    """n bytes, ready for a first call: zero-filled where they must be.  (A few
+    MB cost less to clear than the slice does.)"""
+    if n <= 1 << 22:
+        return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:WORKSPACE_ZERO_BYTES].zero_()
+    return ws
+
+
 def decode_tree_workspace(q, k_cache):
-    """A zero-filled device workspace for decode_tree on these shapes (reusable
-    by later calls of any shape that fits)."""
+    """A device workspace for decode_tree on these shapes, ready for its first
+    use (and for later calls of any shape that fits)."""
     B, Hq, t, d = q.shape
     code = _dtype_code(q)
     n = lib().gqa_decode_tree_workspace_bytes(code, B, Hq, k_cache.shape[1], k_cache.shape[2], d, t)
-    # zero-filled once; every completed call leaves it ready for the next
-    return torch.zeros(max(n, 256), dtype=torch.uint8, device=q.device)
+    return _workspace(n, q.device)  # every completed call leaves it ready for the next
 
 
 def decode_tree(q, k_cache, v_cache, k_draft, v_draft, parents, seq_lens, *, window=None,
@@ -560,13 +570,12 @@ def tree_commit(k_cache, v_cache, k_draft, v_draft, path, path_lens, seq_lens, *
 
 
 def decode_scored_workspace(q, k_cache):
-    """A zero-filled device workspace for decode_scored on these shapes
-    (reusable by later calls of any shape that fits)."""
+    """A device workspace for decode_scored on these shapes, ready for its first
+    use (and for later calls of any shape that fits)."""
     B, Hq, t, d = q.shape if q.dim() == 4 else (*q.shape[:2], 1, q.shape[2])
     code = _dtype_code(q)
     n = lib().gqa_decode_scored_workspace_bytes(code, B, Hq, k_cache.shape[1], k_cache.shape[2], d, t)
-    # zero-filled once; every completed call leaves it ready for the next
-    return torch.zeros(max(n, 256), dtype=torch.uint8, device=q.device)
+    return _workspace(n, q.device)  # every completed call leaves it ready for the next
 
 
 def decode_scored(q, k_cache, v_cache, weights, seq_lens, *, scale=None, out=None, workspace=None,

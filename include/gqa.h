@@ -358,6 +358,10 @@ gqa_status gqa_qk_norm_rope(gqa_dtype dtype, const void *qkv, int64_t batch_stri
 /* Most drafted tokens (or scored rows) per sequence. */
 #define GQA_MAX_TREE 128
 
+/* Of a workspace, what must be zero before its first use: this many bytes at
+ * its start (the counters).  The rest needs no initial value. */
+#define GQA_WORKSPACE_ZERO_BYTES ((size_t)4352)
+
 /*
  * gqa_decode_tree -- attention for a tree of drafted tokens over a cache.
  * [P1] "Extend the existing full and cached attention paths": candidate rows
@@ -378,9 +382,10 @@ gqa_status gqa_qk_norm_rope(gqa_dtype dtype, const void *qkv, int64_t batch_stri
  *   window   as elsewhere, counted in positions: a node at depth m reads
  *            cells >= seq_lens[b] + m - (w - 1) and its last w - 1 ancestors
  *   workspace  gqa_decode_tree_workspace_bytes(...) bytes, 256-byte aligned,
- *            with gqa_decode's rules: zero-filled once before its first use,
- *            left ready for the next call of any shape by every call that
- *            completes, zeroed again after GQA_ERR_TIMEOUT; calls sharing it
+ *            with gqa_decode's rules: zero-filled once before its first use
+ *            (its first GQA_WORKSPACE_ZERO_BYTES are enough), left ready for
+ *            the next call of any shape by every call that completes, zeroed
+ *            again after GQA_ERR_TIMEOUT; calls sharing it
  *            must be ordered (calls of gqa_decode and its relatives, of
  *            gqa_decode_tree and of gqa_decode_scored may share one)
  *   dev_status device int32 (required)
@@ -433,8 +438,11 @@ gqa_status gqa_tree_commit(gqa_dtype dtype, void *k_cache, void *v_cache, const 
  *   weights  device float [B,Hkv,C], in/out; cells >= n_b are left alone
  *   seq_lens device int32 [B], n_b in [t_new, C]
  *   workspace  gqa_decode_scored_workspace_bytes(...) bytes, 256-byte
- *            aligned, with the rules of gqa_decode_tree's (with few rows
- *            it holds the scores: 4 bytes per query row and cell)
+ *            aligned, with the rules of gqa_decode_tree's.  It holds the
+ *            scores, 4 bytes per query row and cell, unless the tensors are
+ *            bf16 with d in {64, 128} and a KV group has more than d / 4 rows
+ *            (Hq / Hkv * t_new) and more than one new row; then its size does
+ *            not depend on C
  * A length outside [t_new, C] sets GQA_ERR_CAPACITY, zeroes that sequence's
  * output and leaves its weights.  t_new > GQA_MAX_TREE returns
  * GQA_ERR_UNSUPPORTED.
