@@ -73,8 +73,10 @@ bool layout(gqa_dtype dtype, int B, int Hq, int Hkv, int C, int d, int t, bool s
   L.scores = scored && !(tc_type && R > d / 4);
   // One scored row is a decode step: its kernel reads the cache at the same
   // rate and has a tenth of the tile kernel's fixed costs (B = 8, 8001 cells:
-  // 59 us with tiles of 128 rows).
-  L.dec = L.tc && scored && t == 1 && gqa::dechost::splitk_rows_ok(B, Hkv, C);
+  // 59 us with tiles of 128 rows).  Within that kernel's limits, those of
+  // gqa_decode; the tiles have none of them.
+  L.dec = L.tc && scored && t == 1 && gqa::dechost::splitk_rows_ok(B, Hkv, C) && B <= 65535 &&
+          gqa::dechost::decode_plan(Hq, Hkv).VL <= 65535;
   if (L.dec) {
     gqa::dechost::DecLayout D;
     if (!gqa::dechost::decode_layout(B, Hq, Hkv, d, &D)) return false;
@@ -203,7 +205,6 @@ gqa_status launch_simt(Params p, const DeviceInfo &di, cudaStream_t st) {
 // One row per sequence on the decode kernel, scores and statistics kept.
 gqa_status launch_dec(const Params &p, const Layout &L, const DeviceInfo &di, cudaStream_t st) {
   const gqa::dechost::DecPlan pl = gqa::dechost::decode_plan(p.Hq, p.Hkv);
-  if (pl.VL > 65535 || p.B > 65535) return GQA_ERR_UNSUPPORTED;
   gqa::dec::Params x = {};
   x.q = (const __nv_bfloat16 *)p.q;
   x.o = (__nv_bfloat16 *)p.o;
