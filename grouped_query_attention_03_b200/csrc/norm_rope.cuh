@@ -12,11 +12,13 @@
 //
 // Angles.  Only the angle's fraction of a turn matters, and a far position
 // times a frequency has far more whole turns than fp32 has bits.  Per pair
-// F = frac(inv_freq / 2 pi) as a 64-bit fixed-point fraction (one fp64
-// product); position * F in wrapping 64-bit integers IS the fraction of the
-// angle, exact up to the 2^-53 of F: the error is below |position| * 2^-54
-// turns, and the top 32 bits go to sincospif as a signed half turn in
-// [-1, 1).
+// F = frac(inv_freq / 2 pi) as a 64-bit fixed-point fraction; position * F in
+// wrapping 64-bit integers IS the fraction of the angle, with |position| times
+// F's error.  The quotient is therefore formed in two parts (the rounded fp64
+// product with 1 / 2 pi, and its remainder with the next 53 bits of it): for
+// |inv_freq| up to 2^40 F is within 2^-63.9 turns, the angle of any 32-bit
+// position within 2^-32.9.  Its top 32 bits go to sincospif as a signed half
+// turn in [-1, 1), rounded to fp32 there (2^-25 half turns).
 //
 // Each element is read and written once; what stands between that and the
 // memory's rate is instructions, about 60 for the 16 bytes a lane has of a
@@ -53,11 +55,14 @@ struct Params {
   uint32_t axis[8];  // pair i's axis in bits 2 (i % 16) of word i / 16
 };
 
-// frac(f / 2 pi) * 2^64; the quotient's whole turns are dropped first.
+// frac(f / 2 pi) * 2^64, modulo 2^64.  t - rint(t) is exact; with |f| <= 2^40
+// the rest is below 2^-14 and its own rounding below 2^-67.
 __device__ __forceinline__ uint64_t turn_fraction(float f) {
-  constexpr double kInv2Pi = 0.15915494309189533577;
+  constexpr double kInv2Pi = 0.15915494309189535, kInv2PiLow = -9.839338337591243e-18;
+  constexpr double kTurn = 18446744073709551616.0;
   const double t = (double)f * kInv2Pi;
-  return (uint64_t)((t - floor(t)) * 18446744073709551616.0);
+  const double rest = fma((double)f, kInv2PiLow, fma((double)f, kInv2Pi, -t));
+  return (uint64_t)__double2ll_rn((t - rint(t)) * kTurn) + (uint64_t)__double2ll_rn(rest * kTurn);
 }
 
 // The position of token `tok` (b * T + t) that pair i turns by.

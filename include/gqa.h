@@ -331,14 +331,15 @@ gqa_status gqa_cache_append(gqa_dtype dtype, void *k_cache, void *v_cache,
  *            row_stride (in elements, row_stride >= (Hq + 2 Hkv) d)
  *   q_weight, k_weight  [d] of the same type, or NULL: a query (key) head's
  *            row x becomes x / sqrt(mean(x^2) + eps) * weight; NULL leaves it
- *   inv_freq device float [rot_d / 2]: finite frequencies in radians per
- *            position; NULL only when rot_d = 0 (no rotation)
+ *   inv_freq device float [rot_d / 2]: frequencies in radians per position,
+ *            of either sign and up to 2^40; NULL only when rot_d = 0 (no
+ *            rotation)
  *   rot_d    rotated elements of a head, even, <= d; the rest pass
  *   interleaved  0: pair i is elements (i, i + rot_d / 2); else (2i, 2i + 1).
  *            (u, v) becomes (u cos a - v sin a, v cos a + u sin a)
  *   positions  device int32 [axes,B,T], any value, or NULL: position t (one
- *            axis).  a = positions[axis of pair i][b,t] * inv_freq[i], exact
- *            to fp32 at every position
+ *            axis).  a = positions[axis of pair i][b,t] * inv_freq[i], less
+ *            its whole turns, to 2^-23 radians at every position
  *   axes     1 .. 4 position axes (text: 1; images and video: time, height,
  *            width)
  *   pair_axis  HOST int32 [rot_d / 2], each in [0, axes), read during the
