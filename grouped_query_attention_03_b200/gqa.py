@@ -186,6 +186,20 @@ def _stream(stream, device):
     return torch.cuda.current_stream(device).cuda_stream
 
 
+def _alloc(stream, make, *args):
+    """make(*args): what a call allocates itself.  On another stream than the
+    current one its memory has to be that stream's, so that it is cleared, and
+    used again, in the order of the call."""
+    if stream is None:
+        return make(*args)
+    with torch.cuda.stream(stream):
+        return make(*args)
+
+
+def _empty_as(q):
+    return torch.empty_like(q, memory_format=torch.contiguous_format)
+
+
 def _check_lens(lens, B):
     if lens.shape != (B,):
         raise ValueError(f"lengths must be [{B}]")
@@ -204,7 +218,7 @@ def ring_append(k_ring, v_ring, k_new, v_new, seq_lens, *, status=None, stream=N
     if k_new.shape != (B, Hkv, t_new, d) or v_new.shape != k_new.shape:
         raise ValueError("new K/V shape mismatch")
     dev = k_ring.device
-    st = new_status(dev) if status is None else status
+    st = _alloc(stream, new_status, dev) if status is None else status
     _run(dev, "gqa_ring_append", lib().gqa_ring_append,
          _dtype_code(k_ring), _ptr(k_ring, "k_ring"), _ptr(v_ring, "v_ring", k_ring.dtype, dev),
          _ptr(k_new, "k_new", k_ring.dtype, dev), _ptr(v_new, "v_new", k_ring.dtype, dev),
@@ -226,11 +240,11 @@ def ring_decode_append(q, k_ring, v_ring, k_new, v_new, seq_lens, *, scale=None,
     if scale is None:
         scale = d ** -0.5
     if out is None:
-        out = torch.empty_like(q)
+        out = _alloc(stream, torch.empty_like, q)
     dev = q.device
     if workspace is None:
-        workspace = decode_workspace(q, k_ring)
-    st = new_status(dev) if status is None else status
+        workspace = _alloc(stream, decode_workspace, q, k_ring)
+    st = _alloc(stream, new_status, dev) if status is None else status
     _run(dev, "gqa_ring_decode_append", lib().gqa_ring_decode_append,
          _dtype_code(q), _ptr(q, "q"), _ptr(k_ring, "k_ring", q.dtype, dev),
          _ptr(v_ring, "v_ring", q.dtype, dev), _ptr(k_new, "k_new", q.dtype, dev),
@@ -256,7 +270,7 @@ def prefill(q, k, v, *, window=None, scale=None, seq_lens=None, out=None,
     if scale is None:
         scale = d ** -0.5
     if out is None:
-        out = torch.empty_like(q)
+        out = _alloc(stream, torch.empty_like, q)
     dev = q.device
     st = status
     _run(dev, "gqa_prefill", lib().gqa_prefill,
@@ -280,9 +294,9 @@ def prefill_packed(q, k, v, seg_start, *, window=None, scale=None, seq_lens=None
     if scale is None:
         scale = d ** -0.5
     if out is None:
-        out = torch.empty_like(q)
+        out = _alloc(stream, torch.empty_like, q)
     dev = q.device
-    st = new_status(dev) if status is None else status
+    st = _alloc(stream, new_status, dev) if status is None else status
     _run(dev, "gqa_prefill_packed", lib().gqa_prefill_packed,
          _dtype_code(q), _ptr(q, "q"), _ptr(k, "k", q.dtype, dev), _ptr(v, "v", q.dtype, dev),
          _ptr(out, "out", q.dtype, dev), _ptr(seq_lens, "seq_lens", torch.int32, dev),
@@ -318,11 +332,11 @@ def decode(q, k_cache, v_cache, seq_lens, *, window=None, scale=None, out=None,
     if scale is None:
         scale = d ** -0.5
     if out is None:
-        out = torch.empty_like(q)
+        out = _alloc(stream, torch.empty_like, q)
     dev = q.device
     if workspace is None:
-        workspace = decode_workspace(q, k_cache)
-    st = new_status(dev) if status is None else status
+        workspace = _alloc(stream, decode_workspace, q, k_cache)
+    st = _alloc(stream, new_status, dev) if status is None else status
     _run(dev, "gqa_decode", lib().gqa_decode,
          _dtype_code(q), _ptr(q, "q"), _ptr(k_cache, "k_cache", q.dtype, dev),
          _ptr(v_cache, "v_cache", q.dtype, dev), _ptr(out, "out", q.dtype, dev),
@@ -348,11 +362,11 @@ def decode_append(q, k_cache, v_cache, k_new, v_new, seq_lens, *, window=None, s
     if scale is None:
         scale = d ** -0.5
     if out is None:
-        out = torch.empty_like(q)
+        out = _alloc(stream, torch.empty_like, q)
     dev = q.device
     if workspace is None:
-        workspace = decode_workspace(q, k_cache)
-    st = new_status(dev) if status is None else status
+        workspace = _alloc(stream, decode_workspace, q, k_cache)
+    st = _alloc(stream, new_status, dev) if status is None else status
     _run(dev, "gqa_decode_append", lib().gqa_decode_append,
          _dtype_code(q), _ptr(q, "q"), _ptr(k_cache, "k_cache", q.dtype, dev),
          _ptr(v_cache, "v_cache", q.dtype, dev), _ptr(k_new, "k_new", q.dtype, dev),
@@ -375,9 +389,9 @@ def decode_multi(q, k_cache, v_cache, seq_lens, *, window=None, scale=None, out=
     if scale is None:
         scale = d ** -0.5
     if out is None:
-        out = torch.empty_like(q)
+        out = _alloc(stream, torch.empty_like, q)
     dev = q.device
-    st = new_status(dev) if status is None else status
+    st = _alloc(stream, new_status, dev) if status is None else status
     _run(dev, "gqa_decode_multi", lib().gqa_decode_multi,
          _dtype_code(q), _ptr(q, "q"), _ptr(k_cache, "k_cache", q.dtype, dev),
          _ptr(v_cache, "v_cache", q.dtype, dev), _ptr(out, "out", q.dtype, dev),
@@ -399,9 +413,9 @@ def decode_noalloc(q, k_cache, v_cache, seq_lens, *, window=None, scale=None, ou
     if scale is None:
         scale = d ** -0.5
     if out is None:
-        out = torch.empty_like(q)
+        out = _alloc(stream, torch.empty_like, q)
     dev = q.device
-    st = new_status(dev) if status is None else status
+    st = _alloc(stream, new_status, dev) if status is None else status
     _run(dev, "gqa_decode_noalloc", lib().gqa_decode_noalloc,
          _dtype_code(q), _ptr(q, "q"), _ptr(k_cache, "k_cache", q.dtype, dev),
          _ptr(v_cache, "v_cache", q.dtype, dev), _ptr(out, "out", q.dtype, dev),
@@ -419,7 +433,7 @@ def cache_append(k_cache, v_cache, k_new, v_new, seq_lens, *, status=None, strea
     if k_new.shape != (B, Hkv, t_new, d) or v_new.shape != k_new.shape:
         raise ValueError("new K/V shape mismatch")
     dev = k_cache.device
-    st = new_status(dev) if status is None else status
+    st = _alloc(stream, new_status, dev) if status is None else status
     _run(dev, "gqa_cache_append", lib().gqa_cache_append,
          _dtype_code(k_cache), _ptr(k_cache, "k_cache"), _ptr(v_cache, "v_cache", k_cache.dtype, dev),
          _ptr(k_new, "k_new", k_cache.dtype, dev), _ptr(v_new, "v_new", k_cache.dtype, dev),
@@ -461,7 +475,8 @@ def qk_norm_rope(qkv, Hq, Hkv, d, *, q_weight=None, k_weight=None, eps=1e-6, inv
         if w is not None and w.numel() != d:
             raise ValueError(f"{name} must have {d} elements")
     if out is None:
-        out = tuple(torch.empty((B, h, T, d), dtype=dt, device=dev) for h in (Hq, Hkv, Hkv))
+        out = _alloc(stream, lambda: tuple(torch.empty((B, h, T, d), dtype=dt, device=dev)
+                                           for h in (Hq, Hkv, Hkv)))
     q, k, v = out
     rows = (B, Hkv, T, d)
     if q.shape != (B, Hq, T, d) or k.shape != rows or v.shape != rows:
@@ -520,13 +535,13 @@ def decode_tree(q, k_cache, v_cache, k_draft, v_draft, parents, seq_lens, *, win
     if scale is None:
         scale = d ** -0.5
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _alloc(stream, _empty_as, q)
     elif out.shape != shape:
         raise ValueError("out must have the shape of q")
     dev, dt = q.device, q.dtype
     if workspace is None:
-        workspace = decode_tree_workspace(q, k_cache)
-    st = new_status(dev) if status is None else status
+        workspace = _alloc(stream, decode_tree_workspace, q, k_cache)
+    st = _alloc(stream, new_status, dev) if status is None else status
     _run(dev, "gqa_decode_tree", lib().gqa_decode_tree,
          _dtype_code(q), _ptr(q, "q"), _ptr(k_cache, "k_cache", dt, dev),
          _ptr(v_cache, "v_cache", dt, dev), _ptr(k_draft, "k_draft", dt, dev),
@@ -559,7 +574,7 @@ def tree_commit(k_cache, v_cache, k_draft, v_draft, path, path_lens, seq_lens, *
     else:
         _check_lens(lens_out, B)
     dev, dt = k_cache.device, k_cache.dtype
-    st = new_status(dev) if status is None else status
+    st = _alloc(stream, new_status, dev) if status is None else status
     _run(dev, "gqa_tree_commit", lib().gqa_tree_commit,
          _dtype_code(k_cache), _ptr(k_cache, "k_cache"), _ptr(v_cache, "v_cache", dt, dev),
          _ptr(k_draft, "k_draft", dt, dev), _ptr(v_draft, "v_draft", dt, dev),
@@ -594,13 +609,13 @@ def decode_scored(q, k_cache, v_cache, weights, seq_lens, *, scale=None, out=Non
     if scale is None:
         scale = d ** -0.5
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _alloc(stream, _empty_as, q)
     elif out.shape != shape:
         raise ValueError("out must have the shape of q")
     dev, dt = q.device, q.dtype
     if workspace is None:
-        workspace = decode_scored_workspace(q, k_cache)
-    st = new_status(dev) if status is None else status
+        workspace = _alloc(stream, decode_scored_workspace, q, k_cache)
+    st = _alloc(stream, new_status, dev) if status is None else status
     _run(dev, "gqa_decode_scored", lib().gqa_decode_scored,
          _dtype_code(q), _ptr(q, "q"), _ptr(k_cache, "k_cache", dt, dev),
          _ptr(v_cache, "v_cache", dt, dev), _ptr(out, "out", dt, dev),
@@ -639,10 +654,10 @@ def cache_evict(k_cache, v_cache, weights, seq_lens, budget, recent, *, k_out=No
         _check_lens(lens_out, B)
     dev, dt = k_cache.device, k_cache.dtype
     if kept is None:
-        kept = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=dev)
+        kept = _alloc(stream, lambda: torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=dev))
     elif kept.shape != (B, Hkv, budget):
         raise ValueError("kept must be [B,Hkv,budget]")
-    st = new_status(dev) if status is None else status
+    st = _alloc(stream, new_status, dev) if status is None else status
     _run(dev, "gqa_cache_evict", lib().gqa_cache_evict,
          _dtype_code(k_cache), _ptr(k_cache, "k_cache"), _ptr(v_cache, "v_cache", dt, dev),
          _ptr(weights, "weights", torch.float32, dev), _ptr(seq_lens, "seq_lens", torch.int32, dev),
@@ -690,8 +705,8 @@ def selftest_wait_timeout(limit_us, *, arrive=False, device=None, status=None, s
     records GQA_ERR_TIMEOUT) or that one thread completes first (arrive=True:
     both succeed).  Returns (status, gave_up) device tensors."""
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
-    st = new_status(dev) if status is None else status
-    gave_up = torch.zeros(2, dtype=torch.int32, device=dev)
+    st = _alloc(stream, new_status, dev) if status is None else status
+    gave_up = _alloc(stream, lambda: torch.zeros(2, dtype=torch.int32, device=dev))
     _run(dev, "gqa_selftest_wait_timeout", lib().gqa_selftest_wait_timeout,
          int(limit_us), 1 if arrive else 0, _ptr(st, "status", torch.int32, dev),
          _ptr(gave_up, "gave_up", torch.int32, dev), _stream(stream, dev))
