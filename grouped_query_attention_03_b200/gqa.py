@@ -584,10 +584,19 @@ def tree_commit(k_cache, v_cache, k_draft, v_draft, path, path_lens, seq_lens, *
     return st
 
 
+def _scored_shape(q):
+    shape = q.shape
+    if len(shape) == 3:
+        return shape[0], shape[1], 1, shape[2]
+    if len(shape) != 4:
+        raise ValueError("q must be [B,Hq,d] or [B,Hq,t,d]")
+    return shape
+
+
 def decode_scored_workspace(q, k_cache):
     """A device workspace for decode_scored on these shapes, ready for its first
     use (and for later calls of any shape that fits)."""
-    B, Hq, t, d = q.shape if q.dim() == 4 else (*q.shape[:2], 1, q.shape[2])
+    B, Hq, t, d = _scored_shape(q)
     code = _dtype_code(q)
     n = lib().gqa_decode_scored_workspace_bytes(code, B, Hq, k_cache.shape[1], k_cache.shape[2], d, t)
     return _workspace(n, q.device)  # every completed call leaves it ready for the next
@@ -598,8 +607,7 @@ def decode_scored(q, k_cache, v_cache, weights, seq_lens, *, scale=None, out=Non
     """decode() (q [B,Hq,d]) or decode_multi() (q [B,Hq,t,d]) that also adds
     to weights [B,Hkv,C] float32 the softmax weights each cell received."""
     shape, cells = q.shape, k_cache.shape
-    B, Hq, d = shape[0], shape[1], shape[-1]
-    t = shape[2] if len(shape) == 4 else 1
+    B, Hq, t, d = _scored_shape(q)
     Hkv, C = cells[1], cells[2]
     if cells != (B, Hkv, C, d) or v_cache.shape != cells:
         raise ValueError("cache shape mismatch")
