@@ -54,8 +54,9 @@
 // SC (gqa_decode_scored, one row): every scaled score also goes to the
 // workspace and each head's merged maximum and 1 / sum beside it, from which
 // another kernel adds up what each cell received.  The sum is then of the
-// fp32 weights (2^-9 of a rounded one would show in fp32 results), and a
-// refused length empties its own sequence only.
+// fp32 weights (the 2^-8 of a rounded one would show in fp32 results; the
+// weights that are multiplied with V are rounded to bf16 all the same), and
+// a refused length empties its own sequence only.
 #pragma once
 
 #include <cuda.h>
@@ -799,7 +800,7 @@ __device__ void consumer(const Params &p, unsigned char *smem,
         }
         const uint32_t p0 = pack_bf16(pv[0], pv[1]);  // row g: heads 2t, 2t + 1
         const uint32_t p1 = pack_bf16(pv[2], pv[3]);  // row g + 8
-        // the denominator sums exactly the bf16 weights the MMA uses
+        // (SC aside) the denominator sums exactly the bf16 weights the MMA uses
         if constexpr (SC) {
           l_run[0] += pv[0] + pv[2];
           l_run[1] += pv[1] + pv[3];
@@ -885,7 +886,7 @@ __device__ void consumer(const Params &p, unsigned char *smem,
           }
           pa[2 * nt] = pack_bf16(pv[0], pv[1]);
           pa[2 * nt + 1] = pack_bf16(pv[2], pv[3]);
-          // the denominator sums exactly the bf16 weights the MMA uses
+          // (SC aside) the denominator sums exactly the bf16 weights the MMA uses
           if constexpr (SC) {
             l_run[0] += pv[0] + pv[1];
             l_run[1] += pv[2] + pv[3];

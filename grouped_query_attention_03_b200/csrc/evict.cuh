@@ -30,7 +30,9 @@
 // V and walks the rows in ascending order, a chunk loaded completely before
 // it is stored and the next chunk's loads already in flight (they read at or
 // above their own destinations, which are above everything stored so far).
-// Column slices never meet, so this needs no waiting between CTAs.
+// Column slices never meet, so this needs no waiting between CTAs (64 lanes of
+// 8000 cells to 4096: 66 us with the selection, of 42 at the copy rate; 8 of 32768
+// to 4096, 64 CTAs: 27 of 5.5).
 #pragma once
 
 #include "common.cuh"

@@ -14,8 +14,9 @@
 // in the mix) with many rows, by the latency of a step, about 1.5 us, with few.
 // fp32: 4 sequences of 2000 cells, 32 heads of 128 on 8, 32 nodes: 240 us, 18
 // TFLOP/s; one head, 58 cells, 2 nodes: 8.8 us.  Four CTAs per SM (128
-// registers) instead of as many as unlimited registers leave: 240 us against
-// 308 there, 8.8 against 8.6 here.
+// registers, of which the compiler spills 12 to 88 bytes a thread) instead of
+// as many as unlimited registers leave: 240 us against 308 there, 8.8 against
+// 8.6 here.
 #pragma once
 
 #include "rows.cuh"

@@ -26,11 +26,18 @@
 //
 // Bound by HBM with one row tile: a 128-key tile is 4 d * 128 bytes, 1.5 us of
 // an SM's share of the bandwidth at d = 128 (8 sequences of 8000 cells, 26
-// nodes, 32 heads on 8: 56 us, 4.7 TB/s, of which 11 us start and end).  Two
-// row tiles take 2.35 us per 128 keys (1.06 PFLOP/s), each tile's products and
-// softmax in turn with the other's; short segments then show what a segment
-// costs besides its tiles, 7 to 9 us of masks, queries and O's way out (64
-// ragged sequences, 63 nodes, 8 heads on 1: 111 us, 0.6 PFLOP/s).
+// nodes, 32 heads on 8: 57 us, 4.7 TB/s, of which 11 us start and end; 48 ragged
+// sequences to 4000, 16 nodes: 83 us, of 65 at the copy rate; the same with d =
+// 64, where a tile's masks and softmax are as long as at 128: 72 of 32).  Two
+// row tiles take about 2.3 us per 128 keys (1.1 PFLOP/s), each tile's products
+// and softmax in turn with the other's; short segments then show what a
+// segment costs besides its tiles, 7 to 9 us of masks, queries and O's way out
+// (64 ragged sequences, 63 nodes, 8 heads on 1: 104 us, 0.65 PFLOP/s).
+// P enters its product as bf16, since V is (the tensor cores take both operands
+// in one type): one rounding of at most 2^-8 per weight, independent of each
+// other, so an output is off by 2.3e-3 in relative L2 where its own rounding
+// alone makes 1.6e-3; the rows' sums, and what cells received, are of the fp32
+// weights.  The remainders as a second bf16 operand would take a second P V.
 //
 // What a row may not read never reaches it: its scores are masked by a
 // select, and since 0 * NaN is not 0, value rows of an edge tile that some
@@ -53,7 +60,9 @@ constexpr uint32_t kTmemCols = 512;
 constexpr float kLazyRescale = 8.0f;       // log2 units
 constexpr int kTcThreads = 384;
 // Registers per thread after the split: 128 * low + 256 * high must not exceed
-// the 384 threads times the 168 they are launched with.
+// the 384 threads times the 168 they are launched with.  The softmax warps
+// would use more: the compiler spills 142 (NT = 1) to 280 bytes (NT = 2) a
+// thread, which the times above include.
 constexpr int kRegsLow = 72, kRegsHigh = 216;
 static_assert(128 * kRegsLow + 256 * kRegsHigh <= 384 * 168, "register split");
 constexpr int kAddParts = 4;               // parts a CTA adds to its own O at most
@@ -903,7 +912,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           return true;
         };
         // a single pass over the cache evicts itself first, so that parts and
-        // outputs stay in L2; with several groups per lane others read it too
+        // outputs stay in L2; with several groups per lane others read it too.
+        // (Scored rows' keys are read a second time, by another kernel, and
+        // leave all the same.)
         const uint64_t once = p.MG == 1 ? tc::l2_policy_evict_first() : l2_policy_normal();
         int jj = 0, segs = 0, nk = 0, nv = 0;  // tiles, segments, K and V fills so far
         bool ok = true;

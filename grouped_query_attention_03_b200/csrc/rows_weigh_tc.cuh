@@ -4,9 +4,9 @@
 //   weights[b,g,j] += sum over the lane's R rows rho, j <= its cell, of
 //                     2^(s_rho,j - m_rho) / l_rho,   s = scale log2(e) q . k
 // with the rows' m and 1 / l from the attention that ran before.  Reading
-// the keys again (2 d bytes a cell, often still in L2) and multiplying them
-// again costs less than writing and reading R scores of 4 bytes from R = d / 4
-// rows on.
+// the keys again (2 d bytes a cell, from DRAM: the attention lets them go from
+// L2 first) and multiplying them again costs less than writing and reading R
+// scores of 4 bytes from R = d / 4 rows on.
 //
 // The product is taken transposed, S^T = K Q^T: a key per TMEM lane, so its
 // sum over the rows stays in one thread, without shuffles or atomics, and
@@ -18,7 +18,9 @@
 //              buffers of TMEM
 //   warps 4-11 exponentials and sums; the two warpgroups take the tiles in
 //              turn and never wait for each other within a run
-// Bound by the exponentials: 128 x 128 of them per tile and 128 rows.
+// Bound by the exponentials: 128 x 128 of them per tile and 128 rows (8 lanes of
+// 32768 cells, 128 rows of 128: 20 us, of which the exponentials need 7 and the
+// keys' 67 MB 10).
 #pragma once
 
 #include "rows_splitk.cuh"

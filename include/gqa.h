@@ -28,8 +28,11 @@
  * Conventions for every entry point:
  *   - All tensors are contiguous row-major device buffers owned by the
  *     caller.  The library allocates no device memory and keeps no state.
+ *     Outputs overlap no input, except where an entry says that they may.
  *   - Element type: GQA_F32 (float) or GQA_BF16 (bfloat16 storage, fp32
- *     arithmetic).  All tensors of one call share the type.
+ *     arithmetic; where the tensor cores multiply softmax weights with the
+ *     values, the weights are rounded to bfloat16 for it).  All tensors of
+ *     one call share the type.
  *   - Work is enqueued asynchronously on `stream` (a cudaStream_t; NULL is
  *     the legacy default stream).  Host-detectable errors are returned
  *     before anything is enqueued and leave every buffer untouched.
