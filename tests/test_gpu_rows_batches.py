@@ -65,12 +65,13 @@ def test_tree_batches(cuda_lib, case):
     assert int(st.item()) == 0
 
 
-@pytest.mark.parametrize("d", [64, 128])
-def test_unfinite_drafts_stay_in_their_sequence(cuda_lib, d):
+@pytest.mark.parametrize("d,Hkv,t", [(64, 4, 12), (128, 4, 12), (64, 2, 40), (128, 2, 36)])
+def test_unfinite_drafts_stay_in_their_sequence(cuda_lib, d, Hkv, t):
     """inf and NaN in drafted value rows that some nodes read: between the
     segments those rows are added from global memory, while the next lane
-    group's products are already under way."""
-    B, Hq, Hkv, C, t = 45, 8, 4, 800, 12
+    group's products are already under way.  (24 rows, and 160 and 144: two
+    row tiles.)"""
+    B, Hq, C = 45, 8, 800
     lens = lengths(B, C)
     ins = make(B, Hq, Hkv, C, d, t, lens, 31)
     par = random_tree(B, t, 77)
@@ -96,6 +97,33 @@ def test_unfinite_drafts_stay_in_their_sequence(cuda_lib, d):
                     if node in line:
                         assert np.array_equal(got[b, :, i, col], np.full(Hq, bad), equal_nan=True)
                         got[b, :, i, col] = want[b, :, i, col]
+        assert_sequences(torch.from_numpy(got), want, mag)
+
+
+@pytest.mark.parametrize("d,Hkv,t", [(64, 4, 12), (128, 2, 36)])
+def test_unfinite_cells_behind_a_window(cuda_lib, d, Hkv, t):
+    """A cell that the roots' windows still hold and no deeper node's: the roots
+    are not finite, everybody else keeps the bounds."""
+    B, Hq, C, window = 45, 8, 800, 300
+    lens = [max(n, window) for n in lengths(B, C)]
+    ins = make(B, Hq, Hkv, C, d, t, lens, 32)
+    par = random_tree(B, t, 78)
+    for b in range(0, B, 2):
+        ins[2][b, :, lens[b] - (window - 1)] = float("nan") if b % 4 else float("inf")
+    want, mag = so.tree(*[np.nan_to_num(f64(x), nan=0.0, posinf=0.0) for x in ins], par.numpy(), lens,
+                        window=window)
+    dev = [x.to(DEV) for x in ins]
+    lt, pd = torch.tensor(lens, dtype=torch.int32, device=DEV), par.to(DEV)
+    ws = cuda_lib.decode_tree_workspace(dev[0], dev[1])
+    for _ in range(5):
+        st = cuda_lib.new_status(DEV)
+        got = f64(cuda_lib.decode_tree(*dev, pd, lt, window=window, workspace=ws, status=st))
+        assert int(st.item()) == 0
+        for b in range(0, B, 2):
+            for i in range(t):
+                if int(par[b, i]) == -1:
+                    assert not np.isfinite(got[b, :, i]).any(), (b, i)
+                    got[b, :, i] = want[b, :, i]
         assert_sequences(torch.from_numpy(got), want, mag)
 
 
