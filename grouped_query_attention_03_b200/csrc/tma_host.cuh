@@ -2,6 +2,8 @@
 // looked up through the runtime, so the library needs no libcuda link).
 #pragma once
 
+#include <atomic>
+
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -15,19 +17,21 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
                                   CUtensorMapL2promotion,
                                   CUtensorMapFloatOOBfill);
 
+// Looked up until it is found; threads that call for the first time together
+// each look, and store the same.
 inline EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault,
-                                &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-    else
-      cudaGetLastError();
+  static std::atomic<EncodeTiledFn> found{nullptr};
+  EncodeTiledFn fn = found.load(std::memory_order_acquire);
+  if (fn) return fn;
+  void *ptr = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault,
+                              &q) == cudaSuccess &&
+      q == cudaDriverEntryPointSuccess) {
+    fn = reinterpret_cast<EncodeTiledFn>(ptr);
+    found.store(fn, std::memory_order_release);
+  } else {
+    cudaGetLastError();
   }
   return fn;
 }
