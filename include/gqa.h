@@ -36,6 +36,8 @@
  *   - Work is enqueued asynchronously on `stream` (a cudaStream_t; NULL is
  *     the legacy default stream).  Host-detectable errors are returned
  *     before anything is enqueued and leave every buffer untouched.
+ *   - Calls may come from any host thread, from several at once too (each with
+ *     a workspace of its own, or ordered), on the device that is current there.
  *   - `window` is GQA_NO_WINDOW (-1) for plain causal attention, else a
  *     positive cell count that includes the current cell.  0 and values
  *     below -1 return GQA_ERR_WINDOW.
